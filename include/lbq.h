@@ -451,6 +451,119 @@ lbq_status lbq_gather_rows(const void* W_bf16, int n, int k, const int32_t* rows
                            int count, void* out, lbq_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * 8-bit linear layers: frozen weights in 8-bit integers with one scale per
+ * output channel, tokens quantized to 8 bits with one scale per token, and
+ * products in whole numbers.  (The GreenBit article names 1-8 bit kernels; the
+ * pages give no formula for 8 bits.  This is the symmetric row-wise form.)
+ * ---------------------------------------------------------------------------
+ */
+
+/* Element types of the matrices and gradients that take more than one. */
+typedef enum {
+    LBQ_F32 = 0,
+    LBQ_BF16 = 1,
+    LBQ_F16 = 2
+} lbq_dtype;
+
+/* An 8-bit weight.  codes [n, k] in [-127, 127], scale [n] fp32; both
+ * caller-owned DEVICE memory.  n >= 1, k % 16 == 0, 16 <= k <= 131072.
+ * Dequantized value: codes[j, i] * scale[j]. */
+typedef struct {
+    int32_t n, k;
+    int8_t* codes;
+    float* scale;
+} lbq_i8weight;
+
+/*
+ * Quantize the rows of X [rows, k] (dtype: lbq_dtype) to 8 bits:
+ *   amax_i = max_j |x_ij|,  scale_i = fp32(amax_i / 127),
+ *   code_ij = 127 x_ij / amax_i rounded to the nearest integer, ties to even
+ * (of the exact quotient).  A zero row has scale 0 and codes 0.  A row that
+ * holds an infinity or a NaN has scale NaN and codes 0, so that every product
+ * of that row is NaN.  Used for a weight (the rows are output channels: codes
+ * and scale of lbq_i8weight) and for tokens.  k % 16 == 0, k <= 131072.
+ */
+lbq_status lbq_quantize_i8(const void* X, int dtype, int rows, int k, int8_t* codes, float* scale,
+                           lbq_stream_t stream);
+
+/*
+ * Forward of an 8-bit linear layer with a low-rank adapter:
+ *   Xq, sx = the tokens quantized as lbq_quantize_i8 does
+ *   T = X A^T  [m, rank]                                          (fp32, written to T_save)
+ *   Y[t, j] = fp32(sum_i Xq[t, i] codes[j, i]) sx[t] scale[j] + s sum_u T[t, u] B[j, u]   (fp32)
+ * The sum of 8-bit products is exact (int32), so Y does not depend on how the
+ * work is split; the two scales are multiplied in the order written, and the
+ * adapter's term is computed in fp32.  X bf16 [m, k], A bf16 [rank, k], B bf16
+ * [n, rank], T_save fp32 [m, rank], Y fp32 [m, n], all row-major device.
+ * rank == 0 (A, B, T_save may be NULL) has no adapter; 0 <= rank <= 64.
+ * m >= 1; any n.  workspace: lbq_linear_i8_fwd_workspace_size bytes of device
+ * memory with any contents (the tokens' codes and scales); calls that may run
+ * at the same time need separate workspaces.  No output may overlap an input,
+ * the workspace or another output.
+ */
+size_t lbq_linear_i8_fwd_workspace_size(int m, const lbq_i8weight* q, int rank);
+lbq_status lbq_linear_i8_fwd(const void* X, int m, const lbq_i8weight* q, const void* A, const void* B, int rank,
+                             float s, float* Y, float* T_save, void* workspace, size_t workspace_bytes,
+                             lbq_stream_t stream);
+
+/*
+ * Input gradient of the same layer, with the tokens' rounding passed straight
+ * through and the gradient quantized per token as the activations are:
+ *   V = fp32(dY[t, j] * scale[j]);  Vq, sv = V quantized as lbq_quantize_i8 does
+ *   U = dY B  [m, rank]                                           (fp32, written to U_save)
+ *   dX[t, i] = fp32(sum_j Vq[t, j] codes[j, i]) sv[t] + s sum_u U[t, u] A[u, i]           (fp32)
+ * The rounding of V moves dX by at most sv[t] / 2 * sum_j |codes[j, i]| from
+ * dY times the dequantized weight.  The adapter gradients
+ * are lbq_lora_grads on X, dY and the saved T, U.  dY bf16 [m, n]; n % 8 == 0,
+ * n <= 131072.  Same layouts, rank, workspace and overlap rules as the forward.
+ */
+size_t lbq_linear_i8_bwd_workspace_size(int m, const lbq_i8weight* q, int rank);
+lbq_status lbq_linear_i8_bwd(const void* dY, int m, const lbq_i8weight* q, const void* A, const void* B, int rank,
+                             float s, float* dX, float* U_save, void* workspace, size_t workspace_bytes,
+                             lbq_stream_t stream);
+
+/*
+ * One gradient of a list: numel elements of type dtype at g (device), its
+ * scaled copy at out (device; out == g scales in place).  g and out need only
+ * the alignment of their elements (views into flat buffers).  numel may be 0
+ * (g and out are not looked at then).
+ */
+typedef struct {
+    const void* g;
+    void* out;          /* lbq_clip_grad_norm only */
+    int64_t numel;
+    int32_t dtype;      /* lbq_dtype */
+    int32_t reserved;   /* 0 */
+} lbq_grad;
+
+/*
+ * The Euclidean norm of all gradients of a list together, and clipping to
+ * max_norm (the step between the adapter gradients and the optimizer):
+ *   total = sum g^2 over all tensors (fp64),  *norm = fp32(sqrt(total)),
+ *   coef = fp32(min(1, max_norm / (sqrt(total) + 1e-6))),
+ *   out = fp32(g * coef) rounded to the tensor's type.
+ * lbq_grad_norm writes *norm only.  An infinite gradient gives norm inf and
+ * coef 0 (its own element NaN, the finite ones 0), a NaN makes everything NaN:
+ * nothing is skipped silently, and *norm tells.  In place with coef 1 nothing
+ * is written.  max_norm >= 0 and finite.  norm: fp32 [1], device, 16-byte
+ * aligned.  The list is host memory, read before the call returns; any
+ * count >= 1.  An output must not overlap another output or another tensor's
+ * gradient (LBQ_EINVAL); a tensor listed twice counts twice in the norm.
+ * The sums have a fixed order: same tensors, same device, same bits.
+ * workspace: lbq_grad_norm_workspace_size(count) bytes of device memory,
+ * zero-filled before its first use, left ready by every call (after a call
+ * whose kernels timed out, zero it again); calls that may run at the same time
+ * need separate ones.  Errors: LBQ_EINVAL, LBQ_EUNSUPPORTED (dtype), LBQ_EALIGN,
+ * LBQ_EWORKSPACE.
+ */
+size_t lbq_grad_norm_workspace_size(int count);
+lbq_status lbq_grad_norm(const lbq_grad* grads, int count, float* norm, void* workspace, size_t workspace_bytes,
+                         lbq_stream_t stream);
+lbq_status lbq_clip_grad_norm(const lbq_grad* grads, int count, float max_norm, float* norm, void* workspace,
+                              size_t workspace_bytes, lbq_stream_t stream);
+
+/*
  * Test hook for the bounded waits (no counterpart in the source pages): one
  * kernel waits on an mbarrier phase that never completes and then on a
  * device word that nothing sets, each for limit_us microseconds

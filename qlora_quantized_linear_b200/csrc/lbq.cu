@@ -1,6 +1,7 @@
 // lbq.cu -- the C ABI (include/lbq.h): argument validation, tensor-map setup,
 // tile and split selection, and kernel launches.  One translation unit holds
 // every kernel so that the device status word is a single object.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -10,6 +11,9 @@
 #include "dqgemm.cuh"
 #include "dqgemm_bwd.cuh"
 #include "dqgemv.cuh"
+#include "gradclip.cuh"
+#include "i8gemm.cuh"
+#include "i8quant.cuh"
 #include "lora.cuh"
 #include "merge.cuh"
 #include "quantize.cuh"
@@ -156,6 +160,8 @@ bool weights_stable(cudaStream_t st) {
 }
 
 #include "dqgemv_host.cuh"
+#include "i8_host.cuh"
+#include "gradclip_host.cuh"
 
 // Plan of a tensor-core GEMM (forward: 128-row output tiles, reduction over
 // k/64 blocks; backward: 128-feature tiles, reduction over n/64 channel
@@ -1117,6 +1123,116 @@ lbq_status lbq_lora_grads(const void* X, const void* dY, int m, int n, int k, co
     lbq_status st = launch_lora_colgrad(X, m, k, U, rank, s, dA, 1, k, cs);
     if (st != LBQ_OK) return st;
     return launch_lora_colgrad(dY, m, n, T, rank, s, dB, rank, 1, cs);
+}
+
+lbq_status lbq_quantize_i8(const void* X, int dtype, int rows, int k, int8_t* codes, float* scale,
+                           lbq_stream_t stream) {
+    if (!X || !codes || !scale || rows < 1 || k < 16 || k % 16 != 0 || k > kI8MaxReduction) return LBQ_EINVAL;
+    if (!aligned16(X) || !aligned16(codes) || !aligned16(scale)) return LBQ_EALIGN;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    switch (dtype) {
+        case LBQ_F32: return run_i8_quantize<kSrcF32, false>(X, rows, k, nullptr, codes, k, scale, cs);
+        case LBQ_BF16: return run_i8_quantize<kSrcBf16, false>(X, rows, k, nullptr, codes, k, scale, cs);
+        case LBQ_F16: return run_i8_quantize<kSrcF16, false>(X, rows, k, nullptr, codes, k, scale, cs);
+    }
+    return LBQ_EUNSUPPORTED;
+}
+
+size_t lbq_linear_i8_fwd_workspace_size(int m, const lbq_i8weight* q, int rank) {
+    if (m < 1 || rank < 0 || rank > kLoraMaxRank || check_i8weight(q, false) != LBQ_OK) return 0;
+    return i8_tokens(m, q->k).bytes;
+}
+
+size_t lbq_linear_i8_bwd_workspace_size(int m, const lbq_i8weight* q, int rank) {
+    if (m < 1 || rank < 0 || rank > kLoraMaxRank || check_i8weight(q, false) != LBQ_OK) return 0;
+    return i8_tokens(m, q->n).bytes;
+}
+
+lbq_status lbq_linear_i8_fwd(const void* X, int m, const lbq_i8weight* q, const void* A, const void* B, int rank,
+                             float s, float* Y, float* T_save, void* workspace, size_t workspace_bytes,
+                             lbq_stream_t stream) {
+    lbq_status st = check_i8weight(q, true);
+    if (st != LBQ_OK) return st;
+    if (m < 1 || !X || !Y) return LBQ_EINVAL;
+    if (!aligned16(X) || !aligned16(Y)) return LBQ_EALIGN;
+    if ((st = check_lora(rank, A, B, T_save)) != LBQ_OK) return st;
+    const I8Tokens tok = i8_tokens(m, q->k);
+    if (!workspace || workspace_bytes < tok.bytes) return LBQ_EWORKSPACE;
+    if (!aligned16(workspace)) return LBQ_EALIGN;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    int8_t* codes = static_cast<int8_t*>(workspace);
+    float* scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tok.scale_at);
+    if (rank > 0 && (st = launch_lora_rows<false>(X, m, q->k, A, rank, T_save, cs)) != LBQ_OK) return st;
+    if ((st = run_i8_quantize<kSrcBf16, false>(X, m, q->k, nullptr, codes, tok.ld, scale, cs)) != LBQ_OK) return st;
+    I8Job j{q, codes, tok.ld, {}};
+    j.p.m = m;
+    j.p.out = q->n;
+    j.p.red = q->k;
+    j.p.row_scale = scale;
+    j.p.out_scale = q->scale;
+    j.p.rank = rank;
+    j.p.s = s;
+    j.p.T = T_save;
+    j.p.P = static_cast<const uint16_t*>(B);
+    j.p.pj = rank;
+    j.p.pu = 1;
+    j.p.Y = Y;
+    return run_i8_product<false>(j, sm_count(), cs);
+}
+
+lbq_status lbq_linear_i8_bwd(const void* dY, int m, const lbq_i8weight* q, const void* A, const void* B, int rank,
+                             float s, float* dX, float* U_save, void* workspace, size_t workspace_bytes,
+                             lbq_stream_t stream) {
+    lbq_status st = check_i8weight(q, true);
+    if (st != LBQ_OK) return st;
+    if (m < 1 || !dY || !dX || q->n % 8 != 0 || q->n > kI8MaxReduction) return LBQ_EINVAL;
+    if (!aligned16(dY) || !aligned16(dX)) return LBQ_EALIGN;
+    if ((st = check_lora(rank, A, B, U_save)) != LBQ_OK) return st;
+    const I8Tokens tok = i8_tokens(m, q->n);
+    if (!workspace || workspace_bytes < tok.bytes) return LBQ_EWORKSPACE;
+    if (!aligned16(workspace)) return LBQ_EALIGN;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    int8_t* codes = static_cast<int8_t*>(workspace);
+    float* scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tok.scale_at);
+    if (rank > 0 && (st = launch_lora_rows<true>(dY, m, q->n, B, rank, U_save, cs)) != LBQ_OK) return st;
+    if ((st = run_i8_quantize<kSrcBf16, true>(dY, m, q->n, q->scale, codes, tok.ld, scale, cs)) != LBQ_OK) return st;
+    I8Job j{q, codes, tok.ld, {}};
+    j.p.m = m;
+    j.p.out = q->k;
+    j.p.red = q->n;
+    j.p.row_scale = scale;
+    j.p.out_scale = nullptr;
+    j.p.rank = rank;
+    j.p.s = s;
+    j.p.T = U_save;
+    j.p.P = static_cast<const uint16_t*>(A);
+    j.p.pj = 1;
+    j.p.pu = q->k;
+    j.p.Y = dX;
+    return run_i8_product<true>(j, sm_count(), cs);
+}
+
+size_t lbq_grad_norm_workspace_size(int count) { return count < 1 ? 0 : clip_workspace(count); }
+
+static lbq_status grad_norm_call(const lbq_grad* grads, int count, bool clip, float max_norm, float* norm,
+                                 void* workspace, size_t workspace_bytes, lbq_stream_t stream) {
+    if (!norm || !(max_norm >= 0.0f) || std::isinf(max_norm)) return LBQ_EINVAL;
+    const lbq_status st = check_grads(grads, count, clip);
+    if (st != LBQ_OK) return st;
+    if (!aligned16(norm)) return LBQ_EALIGN;
+    if (!workspace || workspace_bytes < clip_workspace(count)) return LBQ_EWORKSPACE;
+    if (!aligned16(workspace)) return LBQ_EALIGN;
+    return run_clip(grads, count, clip, max_norm, norm, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lbq_status lbq_grad_norm(const lbq_grad* grads, int count, float* norm, void* workspace, size_t workspace_bytes,
+                         lbq_stream_t stream) {
+    return grad_norm_call(grads, count, false, 0.0f, norm, workspace, workspace_bytes, stream);
+}
+
+lbq_status lbq_clip_grad_norm(const lbq_grad* grads, int count, float max_norm, float* norm, void* workspace,
+                              size_t workspace_bytes, lbq_stream_t stream) {
+    return grad_norm_call(grads, count, true, max_norm, norm, workspace, workspace_bytes, stream);
 }
 
 #ifdef LBQ_TRACE

@@ -22,6 +22,9 @@ That sum is the only exchange on this path: rank * (k + n) * 4 bytes per layer
 flat fp32 buffer, so a step makes ONE all-reduce (NCCL over NVLink/NVSwitch on
 GPUs; gloo on CPUs), issued after the last layer's gradient kernels on the
 same stream.  Nothing else crosses ranks: the frozen weights are replicated.
+With `max_grad_norm` the step then clips all adapters' gradients together
+(lbq_clip_grad_norm on the flat buffer): the buffer is the same on every rank
+after the all-reduce, so the ranks agree on the norm without another exchange.
 
 The per-rank products run in the library's CUDA kernels.  `grad_fn` replaces
 them only where a test supplies its own per-rank computation (the CPU tests of
@@ -35,8 +38,9 @@ from typing import Callable, List, Optional, Sequence
 class AdapterLayer:
     """One frozen quantized weight with its trainable adapter.
 
-    qw: a `lbq.QuantizedWeight` (or any object with n, k); A: bf16 [rank, k];
-    B: bf16 [n, rank]; s: adapter scale."""
+    qw: a `lbq.QuantizedWeight`, a `lbq.Int8Weight` (lbq_linear_i8_fwd and
+    lbq_linear_i8_bwd) or any object with n, k; A: bf16 [rank, k]; B: bf16
+    [n, rank]; s: adapter scale."""
 
     def __init__(self, qw, A, B, s: float):
         self.qw, self.A, self.B, self.s = qw, A, B, float(s)
@@ -50,10 +54,13 @@ class DataParallelQLoRA:
     """The data-parallel step over a list of AdapterLayer.
 
     group: a torch.distributed process group (None: the default group when
-    torch.distributed is initialised, else a single process)."""
+    torch.distributed is initialised, else a single process).
+    max_grad_norm: clip the gradients of all adapters together to this
+    Euclidean norm after the all-reduce (None: no clipping); `grad_norm` holds
+    the norm before, fp32 [1] on the device."""
 
     def __init__(self, layers: Sequence[AdapterLayer], group=None, average: bool = False,
-                 grad_fn: Optional[Callable] = None, device=None):
+                 grad_fn: Optional[Callable] = None, device=None, max_grad_norm: Optional[float] = None):
         import torch
         self.torch = torch
         self.layers: List[AdapterLayer] = list(layers)
@@ -70,6 +77,11 @@ class DataParallelQLoRA:
             off += L.rank * L.k
             L.dB = self.flat[off:off + L.n * L.rank].view(L.n, L.rank)
             off += L.n * L.rank
+        self.max_grad_norm = None if max_grad_norm is None else float(max_grad_norm)
+        self.grad_norm = None
+        if self.max_grad_norm is not None:
+            from . import lbq
+            self._clip = lbq.GradClip([self.flat])
 
     # ------------------------------------------------------------------ ranks
     def _dist(self):
@@ -94,8 +106,10 @@ class DataParallelQLoRA:
                 L.dB.copy_(dB)
             else:
                 from . import lbq
-                Y, T = lbq.linear_fwd(X, L.qw, L.A, L.B, L.s, stream=stream)
-                dX, U = lbq.linear_bwd(dY, L.qw, L.A, L.B, L.s, stream=stream)
+                i8 = isinstance(L.qw, lbq.Int8Weight)
+                fwd, bwd = (lbq.linear_i8_fwd, lbq.linear_i8_bwd) if i8 else (lbq.linear_fwd, lbq.linear_bwd)
+                Y, T = fwd(X, L.qw, L.A, L.B, L.s, stream=stream)
+                dX, U = bwd(dY, L.qw, L.A, L.B, L.s, stream=stream)
                 lbq.lora_grads(X, dY, T, U, L.s, dA=L.dA, dB=L.dB, stream=stream)
             outs.append((Y, dX))
         return outs
@@ -119,10 +133,17 @@ class DataParallelQLoRA:
             if self.average:
                 self.flat.div_(d.get_world_size(self.group))
 
+    def clip(self, stream=None):
+        """Clip the adapters' gradients to max_grad_norm (nothing without one);
+        after the all-reduce, on the same stream."""
+        if self.max_grad_norm is not None:
+            self.grad_norm = self._clip.clip(self.max_grad_norm, stream=stream)
+
     def step(self, shards, stream=None):
-        """local_step then all_reduce; returns the per-layer (Y_r, dX_r)."""
+        """local_step, all_reduce, clip; returns the per-layer (Y_r, dX_r)."""
         outs = self.local_step(shards, stream=stream)
         self.all_reduce(stream=stream)
+        self.clip(stream=stream)
         return outs
 
     def grads(self):

@@ -27,6 +27,7 @@ _L = ctypes.CDLL(LIB_PATH)
 
 LBQ_OK, LBQ_EINVAL, LBQ_EALIGN, LBQ_EUNSUPPORTED, LBQ_ECUDA, LBQ_ETIMEOUT, LBQ_EWORKSPACE = range(7)
 LBQ_MINMAX_ASYM, LBQ_CODEBOOK4 = 0, 1
+LBQ_F32, LBQ_BF16, LBQ_F16 = 0, 1, 2
 STATUS_TIMEOUT, STATUS_BAD_TABLE = 1, 2
 
 
@@ -65,11 +66,21 @@ class lbq_mix_problem(ctypes.Structure):
                 ("Y", ctypes.c_void_p), ("T_save", ctypes.c_void_p)]
 
 
+class lbq_i8weight(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("k", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class lbq_grad(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _vp, _int, _f32, _sz, _u32p = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(ctypes.c_uint32)
 _QP, _MP = ctypes.POINTER(lbq_qweight), ctypes.POINTER(lbq_qweight_mix)
 _PP, _QPP, _I64P = ctypes.POINTER(lbq_fwd_problem), ctypes.POINTER(ctypes.POINTER(lbq_qweight)), ctypes.POINTER(ctypes.c_int64)
 _BPP = ctypes.POINTER(lbq_bwd_problem)
 _MPP = ctypes.POINTER(lbq_mix_problem)
+_IP, _GP = ctypes.POINTER(lbq_i8weight), ctypes.POINTER(lbq_grad)
 _SIGS = {
     "lbq_status_string": (ctypes.c_char_p, [_int]),
     "lbq_quantize_workspace_size": (_sz, [_QP]),
@@ -98,6 +109,14 @@ _SIGS = {
     "lbq_selftest_wait_timeout": (_int, [ctypes.c_uint32, _vp]),
     "lbq_linear_fwd_mix_grouped_workspace_size": (_sz, [_int, _MPP, _int]),
     "lbq_linear_fwd_mix_grouped": (_int, [_int, _MPP, _int, _vp, _sz, _vp]),
+    "lbq_quantize_i8": (_int, [_vp, _int, _int, _int, _vp, _vp, _vp]),
+    "lbq_linear_i8_fwd_workspace_size": (_sz, [_int, _IP, _int]),
+    "lbq_linear_i8_fwd": (_int, [_vp, _int, _IP, _vp, _vp, _int, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "lbq_linear_i8_bwd_workspace_size": (_sz, [_int, _IP, _int]),
+    "lbq_linear_i8_bwd": (_int, [_vp, _int, _IP, _vp, _vp, _int, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "lbq_grad_norm_workspace_size": (_sz, [_int]),
+    "lbq_grad_norm": (_int, [_GP, _int, _vp, _vp, _sz, _vp]),
+    "lbq_clip_grad_norm": (_int, [_GP, _int, _f32, _vp, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_L, _name)
@@ -138,6 +157,14 @@ lbq_gather_rows = _L.lbq_gather_rows
 lbq_selftest_wait_timeout = _L.lbq_selftest_wait_timeout
 lbq_linear_fwd_mix_grouped_workspace_size = _L.lbq_linear_fwd_mix_grouped_workspace_size
 lbq_linear_fwd_mix_grouped = _L.lbq_linear_fwd_mix_grouped
+lbq_quantize_i8 = _L.lbq_quantize_i8
+lbq_linear_i8_fwd_workspace_size = _L.lbq_linear_i8_fwd_workspace_size
+lbq_linear_i8_fwd = _L.lbq_linear_i8_fwd
+lbq_linear_i8_bwd_workspace_size = _L.lbq_linear_i8_bwd_workspace_size
+lbq_linear_i8_bwd = _L.lbq_linear_i8_bwd
+lbq_grad_norm_workspace_size = _L.lbq_grad_norm_workspace_size
+lbq_grad_norm = _L.lbq_grad_norm
+lbq_clip_grad_norm = _L.lbq_clip_grad_norm
 
 
 class LbqError(RuntimeError):
@@ -462,6 +489,188 @@ def unmerge_lora(W, A=None, B=None, s: float = 0.0, out=None, stream=None):
     _check(lbq_unmerge_lora(W.data_ptr(), n, k, _ptr(A) if rank else None, _ptr(B) if rank else None, rank,
                             float(s), out.data_ptr(), _stream(stream)), "lbq_unmerge_lora")
     return out
+
+
+# --------------------------------------------------------------------------- 8-bit linear layers
+def _dtype_code(t, name):
+    torch = _torch()
+    code = {torch.float32: LBQ_F32, torch.bfloat16: LBQ_BF16, torch.float16: LBQ_F16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be fp32, bf16 or fp16, not {t.dtype}")
+    return code
+
+
+def _same_device(dev, **tensors):
+    """The library launches on the current device, so every tensor of a call has to live there."""
+    torch = _torch()
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, not on the current CUDA device")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _out(t, shape, dtype, name, like):
+    """A caller's output, checked, or a new one."""
+    torch = _torch()
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+def quantize_i8(X, codes=None, scale=None, stream=None):
+    """(codes int8 [rows, k], scale fp32 [rows]): the rows of X (fp32, bf16 or fp16) quantized to 8 bits with
+    one symmetric scale per row (lbq_quantize_i8)."""
+    torch = _torch()
+    if X.dim() != 2 or not X.is_cuda or not X.is_contiguous():
+        raise ValueError("X must be a contiguous 2-D CUDA tensor")
+    code = _dtype_code(X, "X")
+    rows, k = X.shape
+    codes = _out(codes, (rows, k), torch.int8, "codes", X)
+    scale = _out(scale, (rows,), torch.float32, "scale", X)
+    _same_device(X.device, codes=codes, scale=scale)
+    _check(lbq_quantize_i8(X.data_ptr(), code, rows, k, codes.data_ptr(), scale.data_ptr(), _stream(stream)),
+           "lbq_quantize_i8")
+    return codes, scale
+
+
+class Int8Weight:
+    """A frozen weight [n, k] in 8-bit integers: codes int8 [n, k] and one fp32 scale per output channel, with
+    their `lbq_i8weight` view.  Fill it with `quantize`, or pass codes and scale that are there already."""
+
+    def __init__(self, n: int, k: int, codes=None, scale=None, device="cuda"):
+        torch = _torch()
+        self.n, self.k = int(n), int(k)
+        if (codes is None) != (scale is None):
+            raise ValueError("codes and scale come together")
+        if codes is None:
+            codes = torch.empty((n, k), dtype=torch.int8, device=device)
+            scale = torch.empty(n, dtype=torch.float32, device=device)
+        self.codes = _out(codes, (self.n, self.k), torch.int8, "codes", codes)
+        self.scale = _out(scale, (self.n,), torch.float32, "scale", scale)
+        if self.codes.device != self.scale.device:
+            raise ValueError("codes and scale must be on one device")
+        self.struct = lbq_i8weight(n=self.n, k=self.k, codes=self.codes.data_ptr(), scale=self.scale.data_ptr())
+        self._ref = ctypes.byref(self.struct)
+
+    def quantize(self, W, stream=None) -> "Int8Weight":
+        if tuple(W.shape) != (self.n, self.k):
+            raise ValueError(f"W must have shape {(self.n, self.k)}")
+        quantize_i8(W, self.codes, self.scale, stream=stream)
+        return self
+
+    def dequantize(self):
+        """fp32 [n, k]: codes times scale."""
+        return self.codes.float() * self.scale[:, None]
+
+
+def linear_i8_fwd_workspace(m: int, qw: Int8Weight, rank: int = 0):
+    """A workspace tensor for linear_i8_fwd with m tokens (any contents; not shared by calls that may overlap)."""
+    torch = _torch()
+    return torch.empty(lbq_linear_i8_fwd_workspace_size(m, qw._ref, rank), dtype=torch.uint8, device=qw.codes.device)
+
+
+def linear_i8_bwd_workspace(m: int, qw: Int8Weight, rank: int = 0):
+    """A workspace tensor for linear_i8_bwd with m tokens (any contents; not shared by calls that may overlap)."""
+    torch = _torch()
+    return torch.empty(lbq_linear_i8_bwd_workspace_size(m, qw._ref, rank), dtype=torch.uint8, device=qw.codes.device)
+
+
+def _linear_i8(call, what, space, x, name, width_in, width_out, qw, A, B, s, out, out_name, saved, saved_name,
+               workspace, stream):
+    torch = _torch()
+    x = _bf16_2d(x, name)
+    m = x.shape[0]
+    if x.shape[1] != width_in:
+        raise ValueError(f"{name} must have {width_in} columns")
+    if (A is None) != (B is None):
+        raise ValueError("A and B come together")
+    rank = 0
+    if A is not None:
+        A, B, rank = _bf16_2d(A, "A"), _bf16_2d(B, "B"), A.shape[0]
+        if A.shape[1] != qw.k or tuple(B.shape) != (qw.n, rank):
+            raise ValueError(f"A must be [rank, {qw.k}] and B [{qw.n}, rank]")
+    out = _out(out, (m, width_out), torch.float32, out_name, x)
+    saved = _out(saved, (m, rank), torch.float32, saved_name, x) if rank else None
+    if workspace is None:
+        workspace = space(m, qw, rank)
+    _same_device(x.device, codes=qw.codes, A=A, B=B, workspace=workspace, **{out_name: out, saved_name: saved})
+    _check(call(x.data_ptr(), m, qw._ref, _ptr(A), _ptr(B), rank, float(s), out.data_ptr(), _ptr(saved),
+                workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)), what)
+    return out, saved
+
+
+def linear_i8_fwd(X, qw: Int8Weight, A=None, B=None, s: float = 0.0, Y=None, T=None, workspace=None, stream=None):
+    """Y = (Xq Wq^T) sx sw + s (X A^T) B^T with the tokens of X (bf16 [m, k]) quantized to 8 bits in the call;
+    returns (Y fp32 [m, n], T = X A^T fp32 [m, rank] or None)."""
+    return _linear_i8(lbq_linear_i8_fwd, "lbq_linear_i8_fwd", linear_i8_fwd_workspace, X, "X", qw.k, qw.n, qw, A, B, s,
+                      Y, "Y", T, "T", workspace, stream)
+
+
+def linear_i8_bwd(dY, qw: Int8Weight, A=None, B=None, s: float = 0.0, dX=None, U=None, workspace=None, stream=None):
+    """dX = (Vq Wq) sv + s (dY B) A with V = dY times the channel scales, its tokens quantized to 8 bits in the
+    call; returns (dX fp32 [m, k], U = dY B fp32 [m, rank] or None)."""
+    return _linear_i8(lbq_linear_i8_bwd, "lbq_linear_i8_bwd", linear_i8_bwd_workspace, dY, "dY", qw.n, qw.k, qw, A, B,
+                      s, dX, "dX", U, "U", workspace, stream)
+
+
+# --------------------------------------------------------------------------- gradient norm and clipping
+class GradClip:
+    """The norm and the clipping of one list of gradients, step after step: keeps the list's table, the norm and
+    the workspace.  `grads` are contiguous fp32, bf16 or fp16 CUDA tensors; `outs` (default: the gradients
+    themselves) get the scaled copies, with the same types and sizes.  The tensors are held, so their memory
+    stays theirs; calls of one GradClip that may run at the same time race on its workspace."""
+
+    def __init__(self, grads, outs=None):
+        torch = _torch()
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if not self.grads:
+            raise ValueError("no gradients")
+        if len(self.outs) != len(self.grads):
+            raise ValueError("one output for each gradient")
+        dev = self.grads[0].device
+        self.table = (lbq_grad * len(self.grads))()
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if not g.is_contiguous() or not o.is_contiguous():
+                raise ValueError(f"gradient {i} and its output must be contiguous")
+            if o.dtype != g.dtype or o.numel() != g.numel():
+                raise ValueError(f"output {i} must have its gradient's type and size")
+            if g.device != dev or o.device != dev:
+                raise ValueError(f"gradient {i} and its output must be on {dev}")
+            self.table[i] = lbq_grad(g=g.data_ptr(), out=o.data_ptr(), numel=g.numel(),
+                                     dtype=_dtype_code(g, f"gradient {i}"), reserved=0)
+        if dev.type != "cuda":
+            raise ValueError("the gradients must be CUDA tensors")
+        self.total_norm = torch.empty(1, dtype=torch.float32, device=dev)
+        self.workspace = torch.zeros(lbq_grad_norm_workspace_size(len(self.grads)), dtype=torch.uint8, device=dev)
+
+    def norm(self, stream=None):
+        """The Euclidean norm of all gradients together (fp32 [1], on the device)."""
+        _same_device(self.total_norm.device)
+        _check(lbq_grad_norm(self.table, len(self.grads), self.total_norm.data_ptr(), self.workspace.data_ptr(),
+                             self.workspace.numel(), _stream(stream)), "lbq_grad_norm")
+        return self.total_norm
+
+    def clip(self, max_norm: float, stream=None):
+        """Scale the gradients by min(1, max_norm / (norm + 1e-6)); returns their norm before."""
+        _same_device(self.total_norm.device)
+        _check(lbq_clip_grad_norm(self.table, len(self.grads), float(max_norm), self.total_norm.data_ptr(),
+                                  self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)),
+               "lbq_clip_grad_norm")
+        return self.total_norm
+
+
+def grad_norm(grads, stream=None):
+    """The Euclidean norm of all `grads` together (fp32 [1], on the device)."""
+    return GradClip(grads).norm(stream=stream)
+
+
+def clip_grad_norm(grads, max_norm: float, outs=None, stream=None):
+    """Clip `grads` to max_norm, in place or into `outs`; returns their norm before (fp32 [1], on the device)."""
+    return GradClip(grads, outs).clip(max_norm, stream=stream)
 
 
 def device_status() -> int:
