@@ -50,29 +50,53 @@ lbq_status check_i8weight(const lbq_i8weight* q, bool need_data) {
 // ---------------------------------------------------------------------------
 // rows to codes
 // ---------------------------------------------------------------------------
-template <int SRC, bool SCALED>
+template <int SRC, bool SCALED, bool BESIDE>
 lbq_status run_i8_quantize(const void* in, int64_t rows, int64_t len, const float* chan, int8_t* codes, int64_t ldc,
                            float* scale, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>(rows)), one(1, 1, 1);
     const int64_t nvec = len / 8;
+    auto go = [&](auto kern, int threads) {
+        return launch_overlapped(kern, dim3(static_cast<unsigned>(rows)), threads, 0, dim3(1, 1, 1), st, in, len, chan,
+                                 codes, ldc, scale);
+    };
     // the fewest threads that hold the row in registers with up to 32 values each
-    if (nvec <= 256)
-        return launch_overlapped(i8_quantize_rows_kernel<SRC, SCALED, 1, 256>, grid, 256, 0, one, st, in, len, chan,
-                                 codes, ldc, scale);
-    if (nvec <= 512)
-        return launch_overlapped(i8_quantize_rows_kernel<SRC, SCALED, 2, 256>, grid, 256, 0, one, st, in, len, chan,
-                                 codes, ldc, scale);
-    if (nvec <= 1024)
-        return launch_overlapped(i8_quantize_rows_kernel<SRC, SCALED, 4, 256>, grid, 256, 0, one, st, in, len, chan,
-                                 codes, ldc, scale);
-    if (nvec <= 2048)
-        return launch_overlapped(i8_quantize_rows_kernel<SRC, SCALED, 4, 512>, grid, 512, 0, one, st, in, len, chan,
-                                 codes, ldc, scale);
-    if (nvec <= 4096)
-        return launch_overlapped(i8_quantize_rows_kernel<SRC, SCALED, 4, 1024>, grid, 1024, 0, one, st, in, len, chan,
-                                 codes, ldc, scale);
-    return launch_overlapped(i8_quantize_rows_kernel<SRC, SCALED, 0, 1024>, grid, 1024, 0, one, st, in, len, chan,
-                             codes, ldc, scale);
+    if (nvec <= 256) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 1, 256>, 256);
+    if (nvec <= 512) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 2, 256>, 256);
+    if (nvec <= 1024) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 256>, 256);
+    if (nvec <= 2048) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 512>, 512);
+    if (nvec <= 4096) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 1024>, 1024);
+    return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 0, 1024>, 1024);
+}
+
+template <bool COL, int MT, int R8>
+lbq_status launch_i8_adapter(const void* in, int64_t m, int64_t len, const void* wt, int r, float* out, int sms,
+                             cudaStream_t st) {
+    // parts enough for two CTAs per SM
+    const int64_t groups = cdiv(m, MT), chunks = cdiv(len, kAdChunk);
+    const int64_t parts = std::min<int64_t>({kAdMaxParts, chunks, std::max<int64_t>(1, 2 * sms / groups)});
+    return launch_overlapped(i8_adapter_kernel<COL, MT, R8>, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts)),
+                             kAdThreads, AdapterSmem<MT, R8>::kBytes, dim3(1, static_cast<unsigned>(parts), 1), st,
+                             static_cast<const uint16_t*>(in), m, static_cast<int>(len), static_cast<const uint16_t*>(wt), r,
+                             out);
+}
+
+template <bool COL, int MT>
+lbq_status run_i8_adapter(const void* in, int64_t m, int64_t len, const void* wt, int r, float* out, int sms,
+                          cudaStream_t st) {
+    if (r <= 8) return launch_i8_adapter<COL, MT, 1>(in, m, len, wt, r, out, sms, st);
+    if (r <= 16) return launch_i8_adapter<COL, MT, 2>(in, m, len, wt, r, out, sms, st);
+    if (r <= 32) return launch_i8_adapter<COL, MT, 4>(in, m, len, wt, r, out, sms, st);
+    return launch_i8_adapter<COL, MT, 8>(in, m, len, wt, r, out, sms, st);
+}
+
+// Codes and scales of the tokens and, with an adapter, its product `out`.
+template <bool BWD>
+lbq_status run_i8_tokens(const void* in, int64_t m, int64_t len, const float* chan, const void* wt, int r, int8_t* codes,
+                         int64_t ldc, float* scale, float* out, int sms, cudaStream_t st) {
+    if (r == 0) return run_i8_quantize<kSrcBf16, BWD, false>(in, m, len, chan, codes, ldc, scale, st);
+    const lbq_status s = m <= 16 ? run_i8_adapter<BWD, 16>(in, m, len, wt, r, out, sms, st)
+                                 : run_i8_adapter<BWD, 64>(in, m, len, wt, r, out, sms, st);
+    if (s != LBQ_OK) return s;
+    return run_i8_quantize<kSrcBf16, BWD, true>(in, m, len, chan, codes, ldc, scale, st);
 }
 
 // Codes and scales of the tokens in a call's workspace.
@@ -133,7 +157,7 @@ lbq_status launch_i8_pair(const I8Job& j, int sms, cudaStream_t st) {
         return LBQ_ECUDA;
     const int64_t tiles = cdiv(j.p.out, 256) * cdiv(j.p.m, NT);
     const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles, std::max(1, sms / 2)));
-    return launch_overlapped(i8_pair_kernel<NT, TRANS, RP>, dim3(2 * pairs), kI8PairThreads, I8PairCfg<NT>::kBytes,
+    return launch_overlapped(i8_pair_kernel<NT, TRANS, RP>, dim3(2 * pairs), kI8PairThreads, (I8PairCfg<NT, RP>::kBytes),
                              dim3(2, 1, 1), st, tmW, tmX, j.p);
 }
 

@@ -1,0 +1,199 @@
+// i8adapter.cuh -- the adapter's product of an 8-bit layer's call, fp32 [m, r]:
+//
+//   forward   T = X A^T   (A [r, len], rows contiguous along the reduction)
+//   backward  U = dY B    (B [len, r], the rank contiguous)
+//
+// Skinny (r <= 64) and bandwidth-bound.  A CTA takes MT tokens and a part of
+// the reduction, in chunks of 128 through a ring of cp.async stages; its eight
+// warps take 16 of each chunk's 128 steps, so a fragment of the adapter's
+// factor serves all the CTA's tokens.  The products run on mma.sync (bf16 in,
+// fp32 sums); the parts of a token tile form a cluster and are joined over
+// distributed shared memory in a fixed order.  A warp's chain of sums is
+// len / (128 parts) long, which keeps T near the accuracy of an fp32 tree: the
+// adapter's term enters the output in fp32.
+#pragma once
+
+#include "common.cuh"
+#include "lora.cuh"
+
+namespace lbq {
+
+constexpr int kAdThreads = 256;
+constexpr int kAdChunk = 128;
+constexpr int kAdMaxParts = 8;
+
+template <int MT, int R8>
+struct AdapterSmem {
+    static constexpr int kStages = MT <= 16 ? 8 : 4;
+    static constexpr int kRow = kAdChunk * 2 + 16;            // 272 bytes: conflict-free ldmatrix
+    static constexpr int kXBytes = MT * kRow;
+    static constexpr int kWBytes = 8 * R8 * kRow;             // also holds 128 rows of 2 r bytes
+    static constexpr int kStageBytes = kXBytes + kWBytes;
+    static constexpr int kRed = 8 * MT * 8 * R8 * 4;          // the warps' sums reuse the ring
+    static constexpr int kPart = MT * 8 * R8 * 4;             // the CTA's sums, read by the cluster
+    static constexpr int kRing = kStages * kStageBytes > kRed ? kStages * kStageBytes : kRed;
+    static constexpr int kBytes = kRing + kPart;
+    static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
+};
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+// 16 bytes to shared memory, the last 16 - n of them zero (n may be 0).
+__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
+template <bool COL, int MT, int R8>
+__global__ void __launch_bounds__(kAdThreads) i8_adapter_kernel(const uint16_t* __restrict__ in, int64_t m, int len,
+                                                                const uint16_t* __restrict__ wt, int r,
+                                                                float* __restrict__ out) {
+    using L = AdapterSmem<MT, R8>;
+    constexpr int NR = 8 * R8, S = L::kStages, TILES = MT / 16;
+    extern __shared__ __align__(128) uint8_t ad_smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int parts = static_cast<int>(gridDim.y), part = static_cast<int>(blockIdx.y);
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * MT;
+    const int chunks = (len + kAdChunk - 1) / kAdChunk;
+    const int c0 = static_cast<int>(static_cast<int64_t>(chunks) * part / parts);
+    const int nc = static_cast<int>(static_cast<int64_t>(chunks) * (part + 1) / parts) - c0;
+    const uint32_t base = smem_u32(ad_smem);
+    griddep_wait();                 // everything before this kernel is complete ...
+    griddep_launch_dependents();    // ... so what follows may start beside it
+
+    auto load_chunk = [&](int i) {
+        const uint32_t sx = base + (i % S) * L::kStageBytes, sw = sx + L::kXBytes;
+        const int k0 = (c0 + i) * kAdChunk;
+        for (int e = threadIdx.x; e < MT * 16; e += kAdThreads) {
+            const int row = e >> 4, k = k0 + (e & 15) * 8;     // len % 8 == 0: a piece is inside or outside
+            const bool ok = row0 + row < m && k < len;
+            cp_async16_part(sx + row * L::kRow + (e & 15) * 16, ok ? in + (row0 + row) * len + k : in, ok ? 16 : 0);
+        }
+        if (!COL) {
+            for (int e = threadIdx.x; e < NR * 16; e += kAdThreads) {
+                const int t = e >> 4, k = k0 + (e & 15) * 8;
+                const bool ok = t < r && k < len;
+                cp_async16_part(sw + t * L::kRow + (e & 15) * 16, ok ? wt + static_cast<int64_t>(t) * len + k : wt,
+                                ok ? 16 : 0);
+            }
+        } else {
+            // 128 rows of r ranks are one run of 256 r bytes
+            const int have = min(kAdChunk, len - k0) * r * 2;
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(wt + static_cast<int64_t>(k0) * r);
+            for (int e = threadIdx.x; e < kAdChunk * r / 8; e += kAdThreads) {
+                const int n = min(16, max(0, have - e * 16));
+                cp_async16_part(sw + e * 16, n > 0 ? src + e * 16 : reinterpret_cast<const uint8_t*>(wt), n);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    float acc[TILES][R8][4];
+#pragma unroll
+    for (int i = 0; i < TILES; ++i)
+#pragma unroll
+        for (int t = 0; t < R8; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][t][e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        if (i < nc) load_chunk(i);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    const int q = lane >> 3, l8 = lane & 7, kk = warp * 16;
+    for (int i = 0; i < nc; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        __syncthreads();                                       // chunk i landed; chunk i - 1 consumed
+        if (i + S - 1 < nc) load_chunk(i + S - 1);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+        const uint32_t sx = base + (i % S) * L::kStageBytes, sw = sx + L::kXBytes;
+        uint32_t b[R8][2];
+        if (!COL) {
+#pragma unroll
+            for (int t = 0; t < R8; t += 2) {
+                uint32_t f[4];
+                const int row = t * 8 + (R8 > 1 ? (q >> 1) * 8 : 0) + l8;
+                ldmatrix_x4(f, sw + row * L::kRow + (kk + (q & 1) * 8) * 2);
+                b[t][0] = f[0], b[t][1] = f[1];
+                if (R8 > 1) b[t + (R8 > 1)][0] = f[2], b[t + (R8 > 1)][1] = f[3];
+            }
+        } else if ((r & 7) == 0) {
+#pragma unroll
+            for (int t = 0; t < R8; t += 2) {
+                uint32_t f[4];
+                const int u = t * 8 + (R8 > 1 ? (q >> 1) * 8 : 0);
+                // ranks past r are not stored: such a block reads the first one and is dropped
+                ldmatrix_x4_trans(f, sw + ((kk + (q & 1) * 8 + l8) * r + (u < r ? u : 0)) * 2);
+                const bool in0 = t * 8 < r, in1 = t * 8 + 8 < r;
+                b[t][0] = in0 ? f[0] : 0u, b[t][1] = in0 ? f[1] : 0u;
+                if (R8 > 1) b[t + (R8 > 1)][0] = in1 ? f[2] : 0u, b[t + (R8 > 1)][1] = in1 ? f[3] : 0u;
+            }
+        } else {
+            const uint16_t* w = reinterpret_cast<const uint16_t*>(ad_smem + (i % S) * L::kStageBytes + L::kXBytes);
+#pragma unroll
+            for (int t = 0; t < R8; ++t) {
+                const int u = t * 8 + g;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = kk + 8 * h + 2 * c;
+                    b[t][h] = u < r ? static_cast<uint32_t>(w[k * r + u]) | (static_cast<uint32_t>(w[(k + 1) * r + u]) << 16)
+                                    : 0u;
+                }
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < TILES; ++mt) {
+            uint32_t a[4];
+            ldmatrix_x4(a, sx + (mt * 16 + (q & 1) * 8 + l8) * L::kRow + (kk + (q >> 1) * 8) * 2);
+#pragma unroll
+            for (int t = 0; t < R8; ++t) lora_mma(acc[mt][t], a[0], a[1], a[2], a[3], b[t][0], b[t][1]);
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(ad_smem);            // [8 warps][MT][NR]
+    float* sum = reinterpret_cast<float*>(ad_smem + L::kRing); // [MT][NR]
+#pragma unroll
+    for (int mt = 0; mt < TILES; ++mt)
+#pragma unroll
+        for (int t = 0; t < R8; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2*>(red + (warp * MT + mt * 16 + g + 8 * h) * NR + t * 8 + 2 * c) =
+                    make_float2(acc[mt][t][2 * h], acc[mt][t][2 * h + 1]);
+    __syncthreads();
+    for (int e = threadIdx.x; e < MT * NR; e += kAdThreads) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += red[w * MT * NR + e];
+        sum[e] = v;
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int e = threadIdx.x * parts + part; e < MT * NR; e += kAdThreads * parts) {
+        const int row = e / NR, t = e - row * NR;
+        if (t >= r || row0 + row >= m) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int p = 0; p < kAdMaxParts; ++p) {
+            if (p < parts) {
+                uint32_t remote;
+                float x;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(sum + e)), "r"(p));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(remote) : "memory");
+                v += x;
+            }
+        }
+        out[(row0 + row) * r + t] = v;
+    }
+    // the cluster's shared memory stays until all have read it
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+}  // namespace lbq

@@ -306,15 +306,71 @@ __global__ void __launch_bounds__(kI8SplitThreads)
 // ---------------------------------------------------------------------------
 constexpr int kI8PairThreads = 320;       // producer warp, MMA warp, eight epilogue warps
 
-template <int NT>
+// RP: the adapter's rank rounded up to 0, 16 or 64; its factors of a tile are
+// staged in shared memory (T as fp32 [NT][RP + 4], the other factor as bf16
+// [128][RP + 4]: rows that the epilogue's reads meet without bank conflicts).
+template <int NT, int RP>
 struct I8PairCfg {
-    static constexpr int kStages = NT >= 256 ? 6 : 8;
+    static constexpr int kStages = RP > 16 ? 4 : 6;
     static constexpr int kABytes = 128 * 128;
     static constexpr int kBBytes = NT / 2 * 128;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr size_t kBar = size_t(kStages) * kStageBytes;
+    static constexpr int kRow = RP + 4;
+    static constexpr size_t kScale = size_t(kStages) * kStageBytes;          // token scales, fp32 [NT]
+    static constexpr size_t kT = kScale + size_t(NT) * 4;
+    static constexpr size_t kP = kT + (RP > 0 ? size_t(NT) * kRow * 4 : 0);
+    static constexpr size_t kBar = kP + (RP > 0 ? size_t(128) * kRow * 2 : 0);
     static constexpr size_t kBytes = kBar + (2 * kStages + 4) * 8 + 16 + 1024;
+    static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
+
+// 16 lanes x 32 columns of 32 bits, 16 registers: lane (g, c) gets rows g
+// (registers 4 i, 4 i + 1) and g + 8 (4 i + 2, 4 i + 3) at columns 8 i + 2 c
+// and 8 i + 2 c + 1.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// The staged factors of a tile: s T (zero beyond the tokens and the rank) and
+// the other factor of this CTA's 128 output features, by 256 threads.
+template <int NT, int RP>
+__device__ __forceinline__ void i8_stage_factors(const I8Params& p, int64_t j0, int t0, float* sT, uint16_t* sP, int tid) {
+    constexpr int ROW = RP + 4;
+    const int ru = (p.rank + 3) / 4 * 4;
+    if ((p.rank & 3) == 0) {
+        const int q = ru / 4;
+        for (int e = tid; e < NT * q; e += 256) {
+            const int t = e / q, u = (e - t * q) * 4;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (t0 + t < p.m) v = __ldg(reinterpret_cast<const float4*>(p.T + static_cast<int64_t>(t0 + t) * p.rank + u));
+            v.x *= p.s, v.y *= p.s, v.z *= p.s, v.w *= p.s;
+            *reinterpret_cast<float4*>(sT + t * ROW + u) = v;
+        }
+    } else {
+        for (int e = tid; e < NT * ru; e += 256) {
+            const int t = e / ru, u = e - t * ru;
+            sT[t * ROW + u] =
+                (t0 + t < p.m && u < p.rank) ? p.s * __ldg(p.T + static_cast<int64_t>(t0 + t) * p.rank + u) : 0.0f;
+        }
+    }
+    if (p.pj == 1) {                         // the features are contiguous: neighbours to neighbouring threads
+        for (int e = tid; e < 128 * ru; e += 256) {
+            const int u = e >> 7, f = e & 127;
+            sP[f * ROW + u] = (j0 + f < p.out && u < p.rank) ? __ldg(p.P + j0 + f + u * p.pu) : uint16_t(0);
+        }
+    } else {                                 // the ranks are
+        for (int e = tid; e < 128 * ru; e += 256) {
+            const int f = e / ru, u = e - f * ru;
+            sP[f * ROW + u] = (j0 + f < p.out && u < p.rank) ? __ldg(p.P + (j0 + f) * p.pj + u) : uint16_t(0);
+        }
+    }
+}
 
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t smem_addr, uint32_t rank) {
     uint32_t r;
@@ -357,7 +413,7 @@ template <int NT, bool TRANS, int RP>
 __global__ void __launch_bounds__(kI8PairThreads, 1)
     i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ I8Params p) {
-    using C = I8PairCfg<NT>;
+    using C = I8PairCfg<NT, RP>;
     constexpr int S = C::kStages;
     constexpr uint32_t kTmemCols = 2 * NT;
     constexpr uint32_t kIdesc = idesc_i8_s32(256, NT, TRANS);
@@ -473,36 +529,124 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
     } else {
         // ------------------------------------------------------------ epilogue
         griddep_wait();
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int quarter = warp & 3, half = (warp - 2) >> 2, tid = threadIdx.x - 64;
+        float* sx = reinterpret_cast<float*>(smem + C::kScale);
+        float* sT = reinterpret_cast<float*>(smem + C::kT);
+        uint16_t* sP = reinterpret_cast<uint16_t*>(smem + C::kP);
         int n = 0;
         for (int tile = first; tile < tiles; tile += step, ++n) {
             const int buf = n & 1;
-            const int64_t j = static_cast<int64_t>(tile % jtiles) * 256 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
-            const int t0 = (tile / jtiles) * NT + half * (NT / 2);
-            const bool ok = j < p.out;
-            float b[RP > 0 ? RP : 1];
-            i8_load_factor<RP>(p, j, ok, b);
-            const float so = (ok && p.out_scale) ? __ldg(p.out_scale + j) : 1.0f;
-            if (!mbar_wait(&dfull[buf], (n >> 1) & 1, s_abort)) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem + static_cast<uint32_t>(buf * NT + half * (NT / 2)) +
-                                   (static_cast<uint32_t>(quarter * 32) << 16);
+            const int64_t j0 = static_cast<int64_t>(tile % jtiles) * 256 + static_cast<int>(rank) * 128;
+            const int t0 = (tile / jtiles) * NT, h0 = half * (NT / 2);
+            // the tile's scales and factors, while its MMAs run
+            named_barrier_sync(1, 256);
+            if (tid < NT) sx[tid] = t0 + tid < p.m ? __ldg(p.row_scale + t0 + tid) : 0.0f;
+            if (RP > 0) i8_stage_factors<NT, RP>(p, j0, t0, sT, sP, tid);
+            named_barrier_sync(1, 256);
+            const uint32_t taddr = tmem + static_cast<uint32_t>(buf * NT + h0) + (static_cast<uint32_t>(quarter * 32) << 16);
+            const int live = min(NT / 2, p.m - t0 - h0);          // tokens of this warp's half that exist
+            float* y = p.Y + static_cast<int64_t>(t0 + h0) * p.out + j0 + quarter * 32;
+            if (RP == 0) {
+                // lane = output feature: 128 contiguous bytes per token
+                const int64_t j = j0 + quarter * 32 + lane;
+                const bool ok = j < p.out;
+                const float so = (ok && p.out_scale) ? __ldg(p.out_scale + j) : 1.0f;
+                if (!mbar_wait(&dfull[buf], (n >> 1) & 1, s_abort)) continue;   // given up: still meet at the barriers
+                tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < NT / 2; c += 16) {
-                uint32_t r[16];
-                tmem_ld_32x32b_x16(taddr + c, r);
-                tmem_ld_wait();
-                if (c + 16 >= NT / 2) {
-                    // the last columns are in registers: the accumulator is free
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&dempty[buf]), 0));
-                }
-                int acc[16];
+                for (int c = 0; c < NT / 2; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(taddr + c, r);
+                    tmem_ld_wait();
+                    if (c + 16 >= NT / 2) {
+                        // the last columns are in registers: the accumulator is free
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&dempty[buf]), 0));
+                    }
+                    float* row = y + static_cast<int64_t>(c) * p.out + lane;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[i] = static_cast<int>(r[i]);
-                if (ok) i8_store<RP, 16>(p, t0 + c, j, acc, so, b);
-                __syncwarp();
+                    for (int i = 0; i < 16; ++i) {
+                        if (ok && c + i < live) *row = static_cast<float>(static_cast<int>(r[i])) * sx[h0 + c + i] * so;
+                        row += p.out;
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // lane (g, c): four features 8 apart, two tokens of every eight, so that a
+                // value read from shared memory serves several outputs
+                const int g = lane >> 2, c2 = (lane & 3) * 2;
+                const int ru = (p.rank + 3) / 4 * 4;
+                float so[4];
+                bool ok[4];
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int64_t j = j0 + quarter * 32 + 8 * f + g;
+                    ok[f] = j < p.out;
+                    so[f] = (ok[f] && p.out_scale) ? __ldg(p.out_scale + j) : 1.0f;
+                }
+                if (!mbar_wait(&dfull[buf], (n >> 1) & 1, s_abort)) continue;   // given up: still meet at the barriers
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < NT / 2; c += 32) {
+                    uint32_t r[2][16];
+                    tmem_ld_16x256b_x4(taddr + c, r[0]);
+                    tmem_ld_16x256b_x4(taddr + c + (16u << 16), r[1]);
+                    float d[4][4][2];                               // [feature][token group][token]
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) d[f][i][0] = d[f][i][1] = 0.0f;
+                    const float* tr = sT + (h0 + c + c2) * C::kRow;
+                    const uint16_t* pr = sP + (quarter * 32 + g) * C::kRow;
+#pragma unroll 1
+                    for (int u = 0; u < ru; u += 4) {
+                        float b[4][4];
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const uint2 w = *reinterpret_cast<const uint2*>(pr + 8 * f * C::kRow + u);
+                            b[f][0] = __uint_as_float(w.x << 16);
+                            b[f][1] = __uint_as_float(w.x & 0xFFFF0000u);
+                            b[f][2] = __uint_as_float(w.y << 16);
+                            b[f][3] = __uint_as_float(w.y & 0xFFFF0000u);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float4 t = *reinterpret_cast<const float4*>(tr + (8 * i + k) * C::kRow + u);
+#pragma unroll
+                                for (int f = 0; f < 4; ++f) {
+                                    d[f][i][k] = fmaf(t.x, b[f][0], d[f][i][k]);
+                                    d[f][i][k] = fmaf(t.y, b[f][1], d[f][i][k]);
+                                    d[f][i][k] = fmaf(t.z, b[f][2], d[f][i][k]);
+                                    d[f][i][k] = fmaf(t.w, b[f][3], d[f][i][k]);
+                                }
+                            }
+                    }
+                    tmem_ld_wait();
+                    if (c + 32 >= NT / 2) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&dempty[buf]), 0));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 sxv = *reinterpret_cast<const float2*>(sx + h0 + c + 8 * i + c2);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int t = c + 8 * i + c2 + k;
+                            float* row = y + static_cast<int64_t>(t) * p.out + g;
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) {
+                                const int acc = static_cast<int>(r[f >> 1][4 * i + 2 * (f & 1) + k]);
+                                const float v = static_cast<float>(acc) * (k ? sxv.y : sxv.x) * so[f];
+                                if (ok[f] && t < live) row[8 * f] = v + d[f][i][k];
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
             }
         }
     }

@@ -11,6 +11,9 @@
 // value is right unless r lies within 2^-12 of a half-integer.  Those elements
 // (one in about 2^11, and the ties) compare 127 v with the half-integer times
 // amax in fp64, where both products are exact (24 + 8 bits).
+//
+// HBM-bound: a row is read once and stays in registers between its maximum and
+// its codes.
 // A zero row has scale 0 and codes 0.  A row that holds an infinity or a NaN
 // has scale NaN and codes 0, so every product of the row is NaN.
 #pragma once
@@ -45,14 +48,14 @@ __device__ __forceinline__ I8RowScale i8_row_scale(uint32_t amax_bits) {
     return r;
 }
 
-// The code of one value (already multiplied by r.f).
-__device__ __forceinline__ int i8_code(float v, const I8RowScale& r) {
-    const float x = v * r.inv;
-    int c = __float2int_rn(x);                                              // 0 for a NaN (a row without codes)
+// The code of one value (already multiplied by r.f) by the exact comparison.
+__device__ __noinline__ int i8_code_exact(float v, float inv, float a) {
+    const float x = v * inv;
+    int c = __float2int_rn(x);
     if (fabsf(x - static_cast<float>(c)) > 0.5f - 0x1p-12f) {
         const float h = floorf(fabsf(x) + 0x1p-11f - 0.5f) + 0.5f;          // the half-integer next to |x|
         const double p = 127.0 * static_cast<double>(fabsf(v));
-        const double t = static_cast<double>(h) * static_cast<double>(r.a);
+        const double t = static_cast<double>(h) * static_cast<double>(a);
         const int lo = static_cast<int>(h - 0.5f);
         const int m = p > t ? lo + 1 : p < t ? lo : lo + (lo & 1);
         c = v < 0.0f ? -m : m;
@@ -60,13 +63,59 @@ __device__ __forceinline__ int i8_code(float v, const I8RowScale& r) {
     return c;
 }
 
-__device__ __forceinline__ uint32_t pack_i8x4(int a, int b, int c, int d) {
-    return (static_cast<uint32_t>(a) & 0xFFu) | ((static_cast<uint32_t>(b) & 0xFFu) << 8) |
-           ((static_cast<uint32_t>(c) & 0xFFu) << 16) | (static_cast<uint32_t>(d) << 24);
+// The codes of eight values, first in the low byte.  v inv + 1.5 * 2^23 in one
+// fma leaves the rounded integer in the low bits of the sum; the distance of
+// v inv from it, again one fma, tells whether any of the eight is close enough
+// to a half-integer to be looked at exactly.
+__device__ __forceinline__ uint2 i8_codes8(float (&v)[8], const I8RowScale& r) {
+    if (r.inv == 0.0f) return make_uint2(0u, 0u);
+    if (r.f != 1.0f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= r.f;
+    }
+    constexpr float kMagic = 12582912.0f;
+    uint32_t t[8];
+    float far = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float m = fmaf(v[e], r.inv, kMagic);
+        far = fmaxf(far, fabsf(fmaf(v[e], r.inv, kMagic - m)));
+        t[e] = __float_as_uint(m);
+    }
+    if (far > 0.5f - 0x1p-12f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = static_cast<uint32_t>(i8_code_exact(v[e], r.inv, r.a));
+    }
+    return make_uint2(__byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
 }
 
-// Eight consecutive values of a row as fp32, times the channel scales when
-// given (the input gradient folds them into dY; one rounding to fp32).
+// max(m, |v|) that keeps a NaN.
+__device__ __forceinline__ float absmax_nan(float m, float v) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(m), "f"(fabsf(v)));
+    return d;
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4& a, float (&v)[8]) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+// v times eight channel scales, one rounding to fp32 each (the input gradient
+// folds the scales into dY).
+__device__ __forceinline__ void i8_scale8(const float* chan, float (&v)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(chan)), b = __ldg(reinterpret_cast<const float4*>(chan) + 1);
+    v[0] = __fmul_rn(v[0], a.x), v[1] = __fmul_rn(v[1], a.y), v[2] = __fmul_rn(v[2], a.z);
+    v[3] = __fmul_rn(v[3], a.w), v[4] = __fmul_rn(v[4], b.x), v[5] = __fmul_rn(v[5], b.y);
+    v[6] = __fmul_rn(v[6], b.z), v[7] = __fmul_rn(v[7], b.w);
+}
+
+// Eight consecutive values of a row as fp32, times the channel scales when given.
 template <int SRC, bool SCALED>
 __device__ __forceinline__ void i8_load8(const void* row, const float* chan, int64_t j, float (&v)[8]) {
     if (SRC == kSrcF32) {
@@ -76,31 +125,28 @@ __device__ __forceinline__ void i8_load8(const void* row, const float* chan, int
         v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     } else {
         const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + j));
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        if (SRC == kSrcBf16) {
+            unpack_bf16x8(a, v);
+        } else {
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (SRC == kSrcBf16) {
-                v[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            } else {
+            for (int i = 0; i < 4; ++i) {
                 v[2 * i] = f16_bits_to_f32(static_cast<uint16_t>(w[i] & 0xFFFFu));
                 v[2 * i + 1] = f16_bits_to_f32(static_cast<uint16_t>(w[i] >> 16));
             }
         }
     }
-    if (SCALED) {
-        const float4* p = reinterpret_cast<const float4*>(chan + j);
-        const float4 a = __ldg(p), b = __ldg(p + 1);
-        v[0] = __fmul_rn(v[0], a.x), v[1] = __fmul_rn(v[1], a.y), v[2] = __fmul_rn(v[2], a.z);
-        v[3] = __fmul_rn(v[3], a.w), v[4] = __fmul_rn(v[4], b.x), v[5] = __fmul_rn(v[5], b.y);
-        v[6] = __fmul_rn(v[6], b.z), v[7] = __fmul_rn(v[7], b.w);
-    }
+    if (SCALED) i8_scale8(chan + j, v);
 }
 
 // One CTA per row; the row's values stay in registers when it has at most
 // 8 * NV * blockDim.x of them (NV > 0), else they are read twice (NV == 0).
 // len % 8 == 0.
-template <int SRC, bool SCALED, int NV, int THREADS>
+// BESIDE: the kernel before this one (the adapter's product of the same call)
+// started after everything before it was complete and touches nothing of this
+// one's, so the two run side by side; waiting for it comes last, so that the
+// kernel after this one finds both complete.
+template <int SRC, bool SCALED, bool BESIDE, int NV, int THREADS>
 __global__ void __launch_bounds__(THREADS) i8_quantize_rows_kernel(const void* __restrict__ in, int64_t len,
                                                                    const float* __restrict__ chan,
                                                                    int8_t* __restrict__ codes, int64_t ldc,
@@ -108,14 +154,14 @@ __global__ void __launch_bounds__(THREADS) i8_quantize_rows_kernel(const void* _
     constexpr int ESIZE = SRC == kSrcF32 ? 4 : 2;
     constexpr int KEEP = NV > 0 ? NV : 1;
     __shared__ uint32_t s_max[THREADS / 32];
-    griddep_wait();                 // everything before this kernel is complete ...
+    if (!BESIDE) griddep_wait();    // everything before this kernel is complete ...
     griddep_launch_dependents();    // ... so the kernel after it may read what came before
     const int64_t row = blockIdx.x;
     const void* src = static_cast<const uint8_t*>(in) + row * len * ESIZE;
     int8_t* dst = codes + row * ldc;
     const int64_t nvec = len / 8;
     float v[KEEP][8];
-    uint32_t mx = 0u;
+    float top = 0.0f;
     if (NV > 0) {
 #pragma unroll
         for (int i = 0; i < KEEP; ++i) {
@@ -130,27 +176,22 @@ __global__ void __launch_bounds__(THREADS) i8_quantize_rows_kernel(const void* _
 #pragma unroll
         for (int i = 0; i < KEEP; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mx = max(mx, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+            for (int e = 0; e < 8; ++e) top = absmax_nan(top, v[i][e]);
     } else {
         for (int64_t j = threadIdx.x; j < nvec; j += THREADS) {
             i8_load8<SRC, SCALED>(src, chan, j * 8, v[0]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mx = max(mx, __float_as_uint(v[0][e]) & 0x7FFFFFFFu);
+            for (int e = 0; e < 8; ++e) top = absmax_nan(top, v[0][e]);
         }
     }
-    mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+    // the bits of magnitudes order as the magnitudes do, a NaN above infinity
+    uint32_t mx = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top) & 0x7FFFFFFFu);
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
     __syncthreads();
     mx = __reduce_max_sync(0xFFFFFFFFu, (threadIdx.x & 31) < THREADS / 32 ? s_max[threadIdx.x & 31] : 0u);
     const I8RowScale r = i8_row_scale(mx);
     if (threadIdx.x == 0) scale[row] = r.scale;
-    auto put = [&](int64_t j, const float (&x)[8]) {
-        int c[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = i8_code(x[e] * r.f, r);
-        *reinterpret_cast<uint2*>(dst + j * 8) =
-            make_uint2(pack_i8x4(c[0], c[1], c[2], c[3]), pack_i8x4(c[4], c[5], c[6], c[7]));
-    };
+    auto put = [&](int64_t j, float (&x)[8]) { *reinterpret_cast<uint2*>(dst + j * 8) = i8_codes8(x, r); };
     if (NV > 0) {
 #pragma unroll
         for (int i = 0; i < KEEP; ++i) {
@@ -163,6 +204,7 @@ __global__ void __launch_bounds__(THREADS) i8_quantize_rows_kernel(const void* _
             put(j, v[0]);
         }
     }
+    if (BESIDE) griddep_wait();
 }
 
 }  // namespace lbq

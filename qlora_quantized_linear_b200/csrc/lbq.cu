@@ -12,6 +12,7 @@
 #include "dqgemm_bwd.cuh"
 #include "dqgemv.cuh"
 #include "gradclip.cuh"
+#include "i8adapter.cuh"
 #include "i8gemm.cuh"
 #include "i8quant.cuh"
 #include "lora.cuh"
@@ -160,8 +161,6 @@ bool weights_stable(cudaStream_t st) {
 }
 
 #include "dqgemv_host.cuh"
-#include "i8_host.cuh"
-#include "gradclip_host.cuh"
 
 // Plan of a tensor-core GEMM (forward: 128-row output tiles, reduction over
 // k/64 blocks; backward: 128-feature tiles, reduction over n/64 channel
@@ -649,6 +648,9 @@ lbq_status launch_lora_colgrad(const void* in, int64_t m, int64_t ncols, const f
 
 namespace {
 
+#include "i8_host.cuh"
+#include "gradclip_host.cuh"
+
 // The workspace of a channel-mix forward (both halves); ws_budget as for
 // fwd_workspace.
 size_t mix_workspace(int m, const lbq_qweight_mix* q, int sms, size_t ws_budget = ~size_t(0)) {
@@ -1131,9 +1133,9 @@ lbq_status lbq_quantize_i8(const void* X, int dtype, int rows, int k, int8_t* co
     if (!aligned16(X) || !aligned16(codes) || !aligned16(scale)) return LBQ_EALIGN;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     switch (dtype) {
-        case LBQ_F32: return run_i8_quantize<kSrcF32, false>(X, rows, k, nullptr, codes, k, scale, cs);
-        case LBQ_BF16: return run_i8_quantize<kSrcBf16, false>(X, rows, k, nullptr, codes, k, scale, cs);
-        case LBQ_F16: return run_i8_quantize<kSrcF16, false>(X, rows, k, nullptr, codes, k, scale, cs);
+        case LBQ_F32: return run_i8_quantize<kSrcF32, false, false>(X, rows, k, nullptr, codes, k, scale, cs);
+        case LBQ_BF16: return run_i8_quantize<kSrcBf16, false, false>(X, rows, k, nullptr, codes, k, scale, cs);
+        case LBQ_F16: return run_i8_quantize<kSrcF16, false, false>(X, rows, k, nullptr, codes, k, scale, cs);
     }
     return LBQ_EUNSUPPORTED;
 }
@@ -1162,8 +1164,9 @@ lbq_status lbq_linear_i8_fwd(const void* X, int m, const lbq_i8weight* q, const 
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     int8_t* codes = static_cast<int8_t*>(workspace);
     float* scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tok.scale_at);
-    if (rank > 0 && (st = launch_lora_rows<false>(X, m, q->k, A, rank, T_save, cs)) != LBQ_OK) return st;
-    if ((st = run_i8_quantize<kSrcBf16, false>(X, m, q->k, nullptr, codes, tok.ld, scale, cs)) != LBQ_OK) return st;
+    const int sms = sm_count();
+    if ((st = run_i8_tokens<false>(X, m, q->k, nullptr, A, rank, codes, tok.ld, scale, T_save, sms, cs)) != LBQ_OK)
+        return st;
     I8Job j{q, codes, tok.ld, {}};
     j.p.m = m;
     j.p.out = q->n;
@@ -1177,7 +1180,7 @@ lbq_status lbq_linear_i8_fwd(const void* X, int m, const lbq_i8weight* q, const 
     j.p.pj = rank;
     j.p.pu = 1;
     j.p.Y = Y;
-    return run_i8_product<false>(j, sm_count(), cs);
+    return run_i8_product<false>(j, sms, cs);
 }
 
 lbq_status lbq_linear_i8_bwd(const void* dY, int m, const lbq_i8weight* q, const void* A, const void* B, int rank,
@@ -1194,8 +1197,9 @@ lbq_status lbq_linear_i8_bwd(const void* dY, int m, const lbq_i8weight* q, const
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     int8_t* codes = static_cast<int8_t*>(workspace);
     float* scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tok.scale_at);
-    if (rank > 0 && (st = launch_lora_rows<true>(dY, m, q->n, B, rank, U_save, cs)) != LBQ_OK) return st;
-    if ((st = run_i8_quantize<kSrcBf16, true>(dY, m, q->n, q->scale, codes, tok.ld, scale, cs)) != LBQ_OK) return st;
+    const int sms = sm_count();
+    if ((st = run_i8_tokens<true>(dY, m, q->n, q->scale, B, rank, codes, tok.ld, scale, U_save, sms, cs)) != LBQ_OK)
+        return st;
     I8Job j{q, codes, tok.ld, {}};
     j.p.m = m;
     j.p.out = q->k;
@@ -1209,7 +1213,7 @@ lbq_status lbq_linear_i8_bwd(const void* dY, int m, const lbq_i8weight* q, const
     j.p.pj = 1;
     j.p.pu = q->k;
     j.p.Y = dX;
-    return run_i8_product<true>(j, sm_count(), cs);
+    return run_i8_product<true>(j, sms, cs);
 }
 
 size_t lbq_grad_norm_workspace_size(int count) { return count < 1 ? 0 : clip_workspace(count); }
