@@ -6,15 +6,19 @@
 //   out   = g * coef in fp32, rounded to the tensor's type
 //
 // HBM-bound: every gradient is read once for the norm and once more for the
-// scaling.  One persistent CTA per SM walks over 4 KB chunks of all tensors
-// (a warp per chunk), so a launch costs the same for 14 tensors as for 448.
-// Between the two phases the CTAs meet at a grid barrier (a cooperative
-// launch); each warp keeps its first chunks in shared memory meanwhile, and
-// reads the others again from the last backwards, when the L2 cache still
-// holds the latest of them.
+// scaling.  One persistent CTA per SM takes an equal, contiguous range of the
+// 2 KB chunks of all tensors.  The tensors come as kernel arguments; a CTA
+// copies the few that its range meets to shared memory first (walking the
+// arguments where they are costs a constant-cache miss per step: 9 us of a
+// small call).  A warp takes every 32nd chunk of its CTA's range and feeds
+// itself by bulk copies through a ring of its own, so that the loads never wait
+// for the sums (192 KB in flight per SM).  Between the two phases the CTAs meet at a grid barrier (a cooperative
+// launch); what the rings hold by then is scaled without another read, and the
+// rest is read again from the last chunk backwards, the latest of it from L2.
 //
-// The squares of a 16-byte piece are added in fp32 when the sum is in a safe
-// range, else in fp64; the pieces are added in fp64.  Every sum has a fixed
+// The squares of a lane's four 16-byte pieces of a chunk are added in fp32, in
+// chains of four and then in pairs (at most 7 roundings), when the sum is in a
+// safe range, else in fp64; all else is added in fp64.  Every sum has a fixed
 // order (lanes, warps, CTAs), so the norm does not depend on scheduling.
 #pragma once
 
@@ -24,14 +28,15 @@ namespace lbq {
 
 enum GradType : int { kGradF32 = LBQ_F32, kGradBf16 = LBQ_BF16, kGradF16 = LBQ_F16 };
 
-constexpr int kClipThreads = 512;
+constexpr int kClipThreads = 1024;
 constexpr int kClipWarps = kClipThreads / 32;
-constexpr int kClipVecs = 8;                          // 16-byte pieces per lane and chunk
-constexpr int kClipChunk = kClipVecs * 32 * 16;       // 4 KB
-constexpr int kClipKeep = 3;                          // chunks a warp keeps in shared memory
-constexpr int kClipSmem = kClipWarps * kClipKeep * kClipChunk;
-constexpr int kClipMaxCtas = 1024;                    // partial sums in the workspace, per launch
-constexpr int kClipTable = 1000;                      // tensors per launch (kernel arguments are below 32764 bytes)
+constexpr int kClipVecs = 4;                          // 16-byte pieces per lane and chunk
+constexpr int kClipChunk = kClipVecs * 32 * 16;       // 2 KB
+constexpr int kClipSlots = 3;                         // chunks of a warp's ring
+constexpr int kClipRing = kClipWarps * kClipSlots * kClipChunk;
+constexpr uint32_t kClipL2 = 64u << 20;               // bytes of a launch that are held in L2 between the phases
+constexpr int kClipMaxCtas = 256;                     // CTAs of a launch
+constexpr int kClipTable = 976;                       // tensors per launch (kernel arguments are below 32764 bytes)
 
 struct ClipEntry {
     const uint8_t* g;      // rounded down to 16 bytes
@@ -45,9 +50,16 @@ struct ClipEntry {
 template <int CAP>
 struct ClipTable {
     int count;
-    uint32_t chunks;                // of this launch
-    ClipEntry e[CAP];
+    uint32_t chunks;                     // of this launch
+    uint16_t first[kClipMaxCtas + 2];    // the tensor of each CTA's first chunk, then the last tensor
+    alignas(16) ClipEntry e[CAP];
 };
+
+// Shared memory of a CTA: the rings, then the tensors of its range.
+template <int CAP>
+constexpr int clip_smem_bytes() {
+    return kClipRing + CAP * static_cast<int>(sizeof(ClipEntry));
+}
 
 struct ClipWork {
     uint32_t* bar;                  // {arrivals, generation}: arrivals 0 between calls
@@ -67,25 +79,27 @@ __device__ __forceinline__ float grad_f32(uint32_t w, int type, int hi) {
     return type == kGradBf16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(static_cast<uint16_t>(h));
 }
 
-// Sum of the squares of a 16-byte piece.  In fp32 it is safe when it lies in
-// [2^-66, 2^100]: no square overflowed and what squares below the normal
-// range lost is under 2^-60 of it.
-__device__ __forceinline__ double grad_sumsq(const uint4& r, int type) {
+// Sum of the squares of a 16-byte piece in fp32: chains of four.
+__device__ __forceinline__ float grad_sumsq32(const uint4& r, int type) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    float s = 0.0f;
-    if (type == kGradF32) {
+    float s = 0.0f, t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s = fmaf(__uint_as_float(w[i]), __uint_as_float(w[i]), s);
-    } else {
+    for (int i = 0; i < 4; ++i) {
+        const float a = grad_f32(w[i], type, 0);
+        s = fmaf(a, a, s);
+    }
+    if (type != kGradF32) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float a = grad_f32(w[i], type, 0), b = grad_f32(w[i], type, 1);
-            s = fmaf(a, a, s);
-            s = fmaf(b, b, s);
+            const float b = grad_f32(w[i], type, 1);
+            t = fmaf(b, b, t);
         }
     }
-    if (s >= 0x1p-66f && s <= 0x1p100f) return static_cast<double>(s);
-    if ((r.x | r.y | r.z | r.w) == 0u) return 0.0;
+    return s + t;
+}
+
+__device__ __forceinline__ double grad_sumsq64(const uint4& r, int type) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     double d = 0.0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -99,6 +113,23 @@ __device__ __forceinline__ double grad_sumsq(const uint4& r, int type) {
     return d;
 }
 
+// Of a lane's four pieces.  In fp32 it is safe when it lies in [2^-66, 2^100]:
+// no square overflowed and what squares below the normal range lost is under
+// 2^-50 of it.
+__device__ __forceinline__ double grad_sumsq(const uint4 (&r)[4], int type) {
+    const float s = (grad_sumsq32(r[0], type) + grad_sumsq32(r[1], type)) +
+                    (grad_sumsq32(r[2], type) + grad_sumsq32(r[3], type));
+    if (s >= 0x1p-66f && s <= 0x1p100f) return static_cast<double>(s);
+    uint32_t any = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) any |= r[i].x | r[i].y | r[i].z | r[i].w;
+    if (any == 0u) return 0.0;
+    double d = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) d += grad_sumsq64(i == 0 ? r[0] : i == 1 ? r[1] : i == 2 ? r[2] : r[3], type);
+    return d;
+}
+
 __device__ __forceinline__ uint32_t grad_scale_word(uint32_t w, int type, float c) {
     if (type == kGradF32) return __float_as_uint(__fmul_rn(__uint_as_float(w), c));
     const float a = __fmul_rn(grad_f32(w, type, 0), c), b = __fmul_rn(grad_f32(w, type, 1), c);
@@ -106,11 +137,37 @@ __device__ __forceinline__ uint32_t grad_scale_word(uint32_t w, int type, float 
     return static_cast<uint32_t>(f32_to_f16_bits(a)) | (static_cast<uint32_t>(f32_to_f16_bits(b)) << 16);
 }
 
-// The piece at elements [at, at + 16 / size) of a tensor; elements outside
-// [lead, end) read as zero.
-__device__ __forceinline__ uint4 grad_load(const ClipEntry& e, int64_t at) {
-    const int per = e.type == kGradF32 ? 4 : 8;
-    if (at >= e.lead && at + per <= e.end) return __ldcg(reinterpret_cast<const uint4*>(e.g + at * (16 / per)));
+// L2 eviction policies: pieces that are read again in the same launch stay as
+// long as they can, what is not needed again makes room first.
+__device__ __forceinline__ uint64_t l2_policy(bool last) {
+    uint64_t p;
+    if (last) asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    else asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ void bulk_load_hint(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;"
+        ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(pol) : "memory");
+}
+
+// A generic load, also of kernel arguments (which a thread's own index would
+// otherwise read through the constant cache one address at a time).
+__device__ __forceinline__ uint4 ld_generic(const void* p) {
+    uint4 r;
+    asm volatile("ld.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
+}
+
+__device__ __forceinline__ void st_hint(void* a, const uint4& r, uint64_t pol) {
+    asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;"
+                 ::"l"(a), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "l"(pol) : "memory");
+}
+
+// The first or last piece of a tensor that does not fill 16 bytes: elements
+// outside [lead, end) read as zero.
+__device__ __forceinline__ uint4 grad_load_part(const ClipEntry& e, int64_t at) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
     if (e.type == kGradF32) {
 #pragma unroll
@@ -125,25 +182,50 @@ __device__ __forceinline__ uint4 grad_load(const ClipEntry& e, int64_t at) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void grad_store(const ClipEntry& e, int64_t at, const uint4& r) {
-    const int per = e.type == kGradF32 ? 4 : 8;
-    uint8_t* o = e.out + at * (16 / per);
-    if (at >= e.lead && at + per <= e.end && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
-        __stcs(reinterpret_cast<uint4*>(o), r);
-        return;
-    }
+// A piece whose output is not 16-byte aligned or that the tensor does not fill.
+__device__ __forceinline__ void grad_store_part(const ClipEntry& e, int64_t at, const uint4& r) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     if (e.type == kGradF32) {
+        uint32_t* o = reinterpret_cast<uint32_t*>(e.out) + at;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (at + i >= e.lead && at + i < e.end) reinterpret_cast<uint32_t*>(o)[i] = w[i];
+            if (at + i >= e.lead && at + i < e.end) o[i] = w[i];
     } else {
+        uint16_t* o = reinterpret_cast<uint16_t*>(e.out) + at;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (at + i >= e.lead && at + i < e.end)
-                reinterpret_cast<uint16_t*>(o)[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+            if (at + i >= e.lead && at + i < e.end) o[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
     }
 }
+
+// A tensor of the range and what the walk over its chunks needs of it, in
+// registers: neighbouring chunks mostly belong to the same one.
+struct ClipCursor {
+    const ClipEntry* ent;
+    int fn, ti;
+    uint32_t chunk0, next0;     // first chunk of the tensor and of the one after it
+    const uint8_t* g;
+    uint8_t* out;
+    int64_t end;
+    int type, lead, log_per;    // 2^log_per elements in 16 bytes
+    __device__ __forceinline__ ClipCursor(const ClipEntry* e, int n) : ent(e), fn(n), ti(0) { set(); }
+    __device__ __forceinline__ void set() {
+        if (fn < 1) return;
+        const ClipEntry& e = ent[ti];
+        chunk0 = e.chunk0;
+        next0 = ti + 1 < fn ? ent[ti + 1].chunk0 : 0xFFFFFFFFu;
+        g = e.g;
+        out = e.out;
+        end = e.end;
+        type = e.type;
+        lead = e.lead;
+        log_per = type == kGradF32 ? 2 : 3;
+    }
+    __device__ __forceinline__ void seek(uint32_t c) {
+        while (c >= next0) ++ti, set();
+        while (c < chunk0) --ti, set();
+    }
+};
 
 // Sum of one value per thread of the CTA, in a fixed order; valid in all threads.
 __device__ __forceinline__ double cta_sum(double v, double* s_sum) {
@@ -168,35 +250,86 @@ template <int MODE, int CAP>
 __global__ void __launch_bounds__(kClipThreads, 1)
     grad_clip_kernel(const __grid_constant__ ClipTable<CAP> tab, const __grid_constant__ ClipWork wk) {
     extern __shared__ __align__(128) uint8_t clip_smem[];
+    __shared__ uint64_t s_full[kClipWarps][kClipSlots];
     __shared__ double s_sum[kClipWarps];
-    __shared__ int s_last;
+    __shared__ int s_last, s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t nwarps = gridDim.x * kClipWarps;
-    // consecutive chunks go to different SMs
-    const uint32_t c0 = warp * gridDim.x + blockIdx.x;
-    uint4* keep = reinterpret_cast<uint4*>(clip_smem) + warp * kClipKeep * (kClipChunk / 16) + lane;
-    int ti = 0;
-    uint32_t done = 0;                      // chunks this warp has taken
-    griddep_wait();
+    // this CTA's chunks cb .. cb + cn - 1; the warp's are cb + warp + 16 q, q < nq
+    const uint32_t cb = static_cast<uint32_t>(static_cast<uint64_t>(tab.chunks) * blockIdx.x / gridDim.x);
+    const int cn = static_cast<int>(static_cast<uint64_t>(tab.chunks) * (blockIdx.x + 1) / gridDim.x - cb);
+    const int nq = cn > warp ? (cn - 1 - warp) / kClipWarps + 1 : 0;
+    uint8_t* ring = clip_smem + warp * kClipSlots * kClipChunk;
+    uint64_t* full = s_full[warp];
+    if (lane == 0) {
+        for (int i = 0; i < kClipSlots; ++i) mbar_init(&full[i], 1);
+        if (warp == 0) s_abort = 0;
+        fence_mbar_init();
+    }
+    // the tensors of this range, from the arguments to shared memory by all threads at once
+    ClipEntry* ent = reinterpret_cast<ClipEntry*>(clip_smem + kClipRing);
+    const int f0 = tab.first[blockIdx.x], fn = tab.count > 0 ? tab.first[blockIdx.x + 1] - f0 + 1 : 0;
+    if (threadIdx.x < fn) {
+        const uint4* src = reinterpret_cast<const uint4*>(tab.e + f0 + threadIdx.x);
+        uint4* dst = reinterpret_cast<uint4*>(ent + threadIdx.x);
+        dst[0] = ld_generic(src);
+        dst[1] = ld_generic(src + 1);
+    }
+    __syncthreads();
+    const uint64_t drop = l2_policy(false), hold = l2_policy(true);
+    const int held = cn - static_cast<int>(kClipL2 / kClipChunk / gridDim.x);      // first chunk to hold in L2
+    // the whole pieces of chunk q to its slot; piece p of a tensor holds the
+    // elements p << log_per and on
+    ClipCursor tl(ent, fn), tc(ent, fn);    // tensors of the chunk last loaded and of the one worked on
+    auto load = [&](int q) {
+        tl.seek(cb + warp + q * kClipWarps);
+        if (lane == 0) {
+            const int lp = tl.log_per;
+            const int64_t p0 = static_cast<int64_t>(cb + warp + q * kClipWarps - tl.chunk0) * (kClipChunk / 16);
+            const int64_t lo = max(p0, static_cast<int64_t>(tl.lead > 0));
+            const int64_t hi = min(p0 + kClipChunk / 16, tl.end >> lp);
+            const uint32_t bytes = hi > lo ? static_cast<uint32_t>(hi - lo) * 16 : 0;
+            uint64_t* bar = &full[q % kClipSlots];
+            mbar_arrive_expect_tx(bar, bytes);
+            if (bytes)
+                bulk_load_hint(ring + (q % kClipSlots) * kClipChunk + (lo - p0) * 16, tl.g + lo * 16, bytes, bar,
+                               MODE == kClipFused && warp + q * kClipWarps >= held ? hold : drop);
+        }
+    };
+    uint32_t phase = 0;                     // a bit per slot
+    auto wait = [&](int q) {
+        const int slot = q % kClipSlots;
+        mbar_wait(&full[slot], (phase >> slot) & 1u, &s_abort);
+        phase ^= 1u << slot;
+    };
+    // the lane's pieces of chunk q, which begin at element `at` and every 32 pieces on; true when all are whole
+    auto pieces = [&](int q, int64_t at, uint4 (&r)[kClipVecs]) {
+        const uint4* slot = reinterpret_cast<const uint4*>(ring + (q % kClipSlots) * kClipChunk) + lane;
+#pragma unroll
+        for (int i = 0; i < kClipVecs; ++i) r[i] = slot[i * 32];
+        const int64_t first = at - (static_cast<int64_t>(lane) << tc.log_per);
+        if (first >= tc.lead && first + ((kClipChunk / 16) << tc.log_per) <= tc.end) return true;
+        const int per = 1 << tc.log_per;
+#pragma unroll
+        for (int i = 0; i < kClipVecs; ++i) {
+            const int64_t a = at + (i * 32 << tc.log_per);
+            if (a < tc.lead || a + per > tc.end)
+                r[i] = a < tc.end ? grad_load_part(ent[tc.ti], a) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        return false;
+    };
     if (MODE != kClipScale) {
         double acc = 0.0;
-        for (uint32_t c = c0; c < tab.chunks; c += nwarps, ++done) {
-            while (ti + 1 < tab.count && tab.e[ti + 1].chunk0 <= c) ++ti;
-            const ClipEntry& e = tab.e[ti];
-            const int type = e.type, per = type == kGradF32 ? 4 : 8;
-            const int64_t at = (static_cast<int64_t>(c - e.chunk0) * (kClipChunk / 16) + lane) * per;
+        for (int q = 0; q < nq && q < kClipSlots; ++q) load(q);
+        for (int q = 0; q < nq; ++q) {
+            const uint32_t c = cb + warp + q * kClipWarps;
+            tc.seek(c);
+            const int64_t at = static_cast<int64_t>((c - tc.chunk0) * uint64_t(kClipChunk / 16) + lane) << tc.log_per;
+            wait(q);
             uint4 r[kClipVecs];
-#pragma unroll
-            for (int i = 0; i < kClipVecs; ++i) {
-                r[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (at + i * 32 * per < e.end) r[i] = grad_load(e, at + i * 32 * per);
-            }
-#pragma unroll
-            for (int i = 0; i < kClipVecs; ++i) acc += grad_sumsq(r[i], type);
-            if (MODE == kClipFused && done < kClipKeep) {
-#pragma unroll
-                for (int i = 0; i < kClipVecs; ++i) keep[done * (kClipChunk / 16) + i * 32] = r[i];
-            }
+            pieces(q, at, r);
+            __syncwarp();                                       // the slot is read
+            if (q + kClipSlots < nq) load(q + kClipSlots);
+            acc += grad_sumsq(r, tc.type);
         }
         const double mine = cta_sum(acc, s_sum);
         if (threadIdx.x == 0) {
@@ -236,36 +369,29 @@ __global__ void __launch_bounds__(kClipThreads, 1)
     // min(1, x) that keeps a NaN
     const double ratio = static_cast<double>(wk.max_norm) / (norm + 1e-6);
     const float coef = ratio > 1.0 ? 1.0f : static_cast<float>(ratio);
-    if (MODE == kClipScale) {
-        for (uint32_t c = c0; c < tab.chunks; c += nwarps) ++done;
-        ti = tab.count - 1;
-    }
-    while (done > 0) {
-        --done;
-        const uint32_t c = c0 + done * nwarps;
-        while (tab.e[ti].chunk0 > c) --ti;
-        const ClipEntry& e = tab.e[ti];
-        if (coef == 1.0f && e.g == e.out) continue;                    // in place and nothing to change
-        const int type = e.type, per = type == kGradF32 ? 4 : 8;
-        const int64_t at = (static_cast<int64_t>(c - e.chunk0) * (kClipChunk / 16) + lane) * per;
+    if (MODE == kClipScale)
+        for (int q = nq - 1; q >= 0 && q >= nq - kClipSlots; --q) load(q);
+    for (int q = nq - 1; q >= 0; --q) {
+        const uint32_t c = cb + warp + q * kClipWarps;
+        tc.seek(c);
+        const int64_t at = static_cast<int64_t>((c - tc.chunk0) * uint64_t(kClipChunk / 16) + lane) << tc.log_per;
+        if (MODE == kClipScale || q < nq - kClipSlots) wait(q);
         uint4 r[kClipVecs];
+        const bool whole = pieces(q, at, r);
+        __syncwarp();                                           // the slot is read
+        if (q >= kClipSlots) load(q - kClipSlots);
+        if (coef == 1.0f && tc.g == tc.out) continue;           // in place and nothing to change
+        uint8_t* o = tc.out + (at << (4 - tc.log_per));
+        const bool aligned = (reinterpret_cast<uintptr_t>(tc.out) & 15u) == 0;
 #pragma unroll
         for (int i = 0; i < kClipVecs; ++i) {
-            r[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (at + i * 32 * per < e.end) {
-                if (MODE == kClipFused && done < kClipKeep) r[i] = keep[done * (kClipChunk / 16) + i * 32];
-                else r[i] = grad_load(e, at + i * 32 * per);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kClipVecs; ++i) {
-            if (at + i * 32 * per >= e.end) continue;
-            uint4 o;
-            o.x = grad_scale_word(r[i].x, type, coef);
-            o.y = grad_scale_word(r[i].y, type, coef);
-            o.z = grad_scale_word(r[i].z, type, coef);
-            o.w = grad_scale_word(r[i].w, type, coef);
-            grad_store(e, at + i * 32 * per, o);
+            uint4 v;
+            v.x = grad_scale_word(r[i].x, tc.type, coef);
+            v.y = grad_scale_word(r[i].y, tc.type, coef);
+            v.z = grad_scale_word(r[i].z, tc.type, coef);
+            v.w = grad_scale_word(r[i].w, tc.type, coef);
+            if (whole && aligned) st_hint(o + i * 512, v, drop);
+            else grad_store_part(ent[tc.ti], at + (i * 32 << tc.log_per), v);
         }
     }
 }

@@ -78,15 +78,22 @@ lbq_status launch_clip(const lbq_grad* grads, int count, const ClipWork& wk, int
     }
     if (chunks >= (uint64_t(1) << 31)) return LBQ_EUNSUPPORTED;
     tab.chunks = static_cast<uint32_t>(chunks);
+    // the first tensor of each CTA's range (the last that starts at or before the range's first chunk)
+    const int grid = std::min(sms, kClipMaxCtas);
+    for (int b = 0, t = 0; b <= grid; ++b) {
+        const uint64_t c = chunks * b / grid;
+        while (t + 1 < tab.count && tab.e[t + 1].chunk0 <= c) ++t;
+        tab.first[b] = static_cast<uint16_t>(t);
+    }
     auto kern = grad_clip_kernel<MODE, CAP>;
-    const size_t smem = MODE == kClipFused ? kClipSmem : 0;
-    if (smem > 0 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
+    constexpr size_t smem = clip_smem_bytes<CAP>();
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
                         cudaSuccess) {
         (void)cudaGetLastError();
         return LBQ_ECUDA;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min(sms, kClipMaxCtas)));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kClipThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -118,6 +125,9 @@ lbq_status run_clip(const lbq_grad* grads, int count, bool clip, float max_norm,
         if (count <= 64)
             return clip ? launch_clip<kClipFused, 64>(grads, count, wk, sms, st)
                         : launch_clip<kClipSumLast, 64>(grads, count, wk, sms, st);
+        if (count <= 512)
+            return clip ? launch_clip<kClipFused, 512>(grads, count, wk, sms, st)
+                        : launch_clip<kClipSumLast, 512>(grads, count, wk, sms, st);
         return clip ? launch_clip<kClipFused, kClipTable>(grads, count, wk, sms, st)
                     : launch_clip<kClipSumLast, kClipTable>(grads, count, wk, sms, st);
     }

@@ -58,7 +58,7 @@ lbq_status run_i8_quantize(const void* in, int64_t rows, int64_t len, const floa
         return launch_overlapped(kern, dim3(static_cast<unsigned>(rows)), threads, 0, dim3(1, 1, 1), st, in, len, chan,
                                  codes, ldc, scale);
     };
-    // the fewest threads that hold the row in registers with up to 32 values each
+    // the fewest threads that hold the row in registers, up to 64 bytes each
     if (nvec <= 256) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 1, 256>, 256);
     if (nvec <= 512) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 2, 256>, 256);
     if (nvec <= 1024) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 256>, 256);
@@ -79,6 +79,34 @@ lbq_status launch_i8_adapter(const void* in, int64_t m, int64_t len, const void*
                              out);
 }
 
+template <bool COL, int NR>
+lbq_status launch_i8_adapter_tc(const void* in, int64_t m, int64_t len, const void* wt, int r, float* out, int sms,
+                                cudaStream_t st) {
+    CUtensorMap tmX, tmW;
+    if (!make_map_2d(&tmX, in, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, m, len, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+        return LBQ_ECUDA;
+    const bool ok = COL ? make_map_2d(&tmW, wt, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, len, r, 64, NR,
+                                      NR == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                      : NR == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                 : CU_TENSOR_MAP_SWIZZLE_32B)
+                        : make_map_2d(&tmW, wt, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, r, len, NR, 64,
+                                      CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!ok) return LBQ_ECUDA;
+    const int64_t groups = cdiv(m, 128), blocks = cdiv(len, 64);
+    const int64_t parts = std::min<int64_t>({kAdMaxParts, blocks, std::max<int64_t>(1, sms / groups)});
+    return launch_overlapped(i8_adapter_tc_kernel<COL, NR>, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts)),
+                             kAdTcThreads, AdapterTcSmem<NR>::kBytes, dim3(1, static_cast<unsigned>(parts), 1), st, tmX, tmW,
+                             static_cast<int>(m), static_cast<int>(len), r, out);
+}
+
+template <bool COL>
+lbq_status run_i8_adapter_tc(const void* in, int64_t m, int64_t len, const void* wt, int r, float* out, int sms,
+                             cudaStream_t st) {
+    if (r <= 16) return launch_i8_adapter_tc<COL, 16>(in, m, len, wt, r, out, sms, st);
+    if (r <= 32) return launch_i8_adapter_tc<COL, 32>(in, m, len, wt, r, out, sms, st);
+    return launch_i8_adapter_tc<COL, 64>(in, m, len, wt, r, out, sms, st);
+}
+
 template <bool COL, int MT>
 lbq_status run_i8_adapter(const void* in, int64_t m, int64_t len, const void* wt, int r, float* out, int sms,
                           cudaStream_t st) {
@@ -93,8 +121,9 @@ template <bool BWD>
 lbq_status run_i8_tokens(const void* in, int64_t m, int64_t len, const float* chan, const void* wt, int r, int8_t* codes,
                          int64_t ldc, float* scale, float* out, int sms, cudaStream_t st) {
     if (r == 0) return run_i8_quantize<kSrcBf16, BWD, false>(in, m, len, chan, codes, ldc, scale, st);
-    const lbq_status s = m <= 16 ? run_i8_adapter<BWD, 16>(in, m, len, wt, r, out, sms, st)
-                                 : run_i8_adapter<BWD, 64>(in, m, len, wt, r, out, sms, st);
+    const lbq_status s = m <= 16                 ? run_i8_adapter<BWD, 16>(in, m, len, wt, r, out, sms, st)
+                         : !BWD || r % 8 == 0 ? run_i8_adapter_tc<BWD>(in, m, len, wt, r, out, sms, st)
+                                              : run_i8_adapter<BWD, 64>(in, m, len, wt, r, out, sms, st);
     if (s != LBQ_OK) return s;
     return run_i8_quantize<kSrcBf16, BWD, true>(in, m, len, chan, codes, ldc, scale, st);
 }

@@ -14,6 +14,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "dqgemm_bwd.cuh"
 #include "lora.cuh"
 
 namespace lbq {
@@ -193,6 +194,163 @@ __global__ void __launch_bounds__(kAdThreads) i8_adapter_kernel(const uint16_t* 
         out[(row0 + row) * r + t] = v;
     }
     // the cluster's shared memory stays until all have read it
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens: the same product on tcgen05.  A CTA takes 128 tokens and a part
+// of the reduction in blocks of 64, both operands by TMA: the tokens as the
+// K-major A operand, the adapter's factor as the B operand, K-major in the
+// forward and MN-major (the rank contiguous) in the backward, where its rows of
+// 2 r bytes need a multiple of 16 (r % 8 == 0; other ranks take the kernel
+// above).  The MMAs of a block go to several accumulators in turn, which the
+// epilogue adds in fp32: chains of sums in tensor memory stay short.
+// ---------------------------------------------------------------------------
+constexpr int kAdTcThreads = 192;          // producer warp, MMA warp, four epilogue warps
+
+template <int NR>
+struct AdapterTcSmem {
+    static constexpr int kStages = 4;
+    static constexpr int kXBytes = 128 * 128;
+    static constexpr int kWBytes = NR * 128;
+    static constexpr int kStageBytes = kXBytes + kWBytes;
+    static constexpr int kSets = 256 / NR;                     // accumulators of NR columns
+    static constexpr int kRow = NR + 1;                        // the sums of a token, read by the cluster
+    static constexpr size_t kBar = size_t(kStages) * kStageBytes;
+    static constexpr size_t kBytes = kBar + (2 * kStages + 1) * 8 + 16 + 1024;
+    static_assert(size_t(128) * kRow * 4 <= kBar, "the sums reuse the ring");
+};
+
+// MN-major B operand whose rows of NR bf16 fill one swizzle atom (32, 64 or 128
+// bytes): groups of 8 reduction steps are 16 NR bytes apart.
+template <int NR>
+__device__ __forceinline__ uint64_t smem_desc_mn_rank(uint32_t addr) {
+    constexpr uint64_t kLayout = NR == 64 ? 2 : NR == 32 ? 4 : 6;
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1u) << 16) |
+           (static_cast<uint64_t>((16u * NR) >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) | (kLayout << 61);
+}
+
+template <bool COL, int NR>
+__global__ void __launch_bounds__(kAdTcThreads) i8_adapter_tc_kernel(const __grid_constant__ CUtensorMap tmX,
+                                                                     const __grid_constant__ CUtensorMap tmW, int m,
+                                                                     int len, int r, float* __restrict__ out) {
+    using L = AdapterTcSmem<NR>;
+    constexpr int S = L::kStages;
+    constexpr uint32_t kIdesc = idesc_bf16_f32(128, NR) | (COL ? 1u << 16 : 0u);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
+    uint64_t* empty = full + S;
+    uint64_t* dfull = empty + S;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(dfull + 1);
+    volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = static_cast<int>(gridDim.y), part = static_cast<int>(blockIdx.y);
+    const int t0 = static_cast<int>(blockIdx.x) * 128;
+    const int blocks = (len + 63) / 64;
+    const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * part / parts);
+    const int nb = static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / parts) - b0;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(dfull, 1);
+        *s_abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+    }
+    if (warp == 1) {
+        tmem_alloc(s_tmem, 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    griddep_wait();                 // everything before this kernel is complete ...
+    griddep_launch_dependents();    // ... so what follows may start beside it
+    if (warp == 0) {
+        if (lane == 0) {
+            int i = 0;
+            for (; i < nb; ++i) {
+                const int st = i % S;
+                if (i >= S && !mbar_wait(&empty[st], ((i / S) - 1) & 1, s_abort)) break;
+                uint8_t* x = smem + st * L::kStageBytes;
+                mbar_arrive_expect_tx(&full[st], L::kStageBytes);
+                tma_load_2d(x, &tmX, &full[st], (b0 + i) * 64, t0);
+                if (COL) tma_load_2d(x + L::kXBytes, &tmW, &full[st], 0, (b0 + i) * 64);
+                else tma_load_2d(x + L::kXBytes, &tmW, &full[st], (b0 + i) * 64, 0);
+            }
+            for (int d = max(0, i - S); d < i; ++d) mbar_wait_drain(&full[d % S], (d / S) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int i = 0; i < nb; ++i) {
+                const int st = i % S;
+                if (!mbar_wait(&full[st], (i / S) & 1, s_abort)) break;
+                tc_fence_after();
+                const uint32_t x = smem_u32(smem + st * L::kStageBytes), w = x + L::kXBytes;
+                const uint32_t d = tmem + static_cast<uint32_t>((i % L::kSets) * NR);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mma_ss(d, smem_desc_k_sw128(x) + static_cast<uint64_t>(2 * j),
+                           COL ? smem_desc_mn_rank<NR>(w + j * 32 * NR) : smem_desc_k_sw128(w) + static_cast<uint64_t>(2 * j),
+                           kIdesc, (i >= L::kSets || j > 0) ? 1u : 0u);
+                mma_commit(&empty[st]);
+            }
+            mma_commit(dfull);
+            mbar_wait_drain(dfull, 0);
+        }
+    } else {
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        const bool done = mbar_wait(dfull, 0, s_abort);
+        tc_fence_after();
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        float* sum = reinterpret_cast<float*>(smem) + row * L::kRow;
+        const int sets = min(nb, L::kSets);
+#pragma unroll 1
+        for (int c = 0; done && c < NR; c += 16) {
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+            for (int k = 0; k < sets; ++k) {
+                uint32_t a[16];
+                tmem_ld_32x32b_x16(taddr + k * NR + c, a);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(a[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[c + e] = v[e];
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
+    }
+    const int live = min(128, m - t0);
+    for (int e = threadIdx.x * parts + part; e < live * r; e += kAdTcThreads * parts) {
+        const int row = e / r, t = e - row * r;
+        const uint32_t at = smem_u32(smem) + (row * L::kRow + t) * 4;
+        float v = 0.0f;
+#pragma unroll
+        for (int p = 0; p < kAdMaxParts; ++p) {
+            if (p < parts) {
+                uint32_t remote;
+                float x;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(p));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(remote) : "memory");
+                v += x;
+            }
+        }
+        out[static_cast<int64_t>(t0) * r + e] = v;
+    }
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
