@@ -4,14 +4,26 @@
 
 // Launch with optional cluster size and programmatic stream serialisation
 // (the kernel waits with griddepcontrol.wait before it reads what the kernel
-// before it wrote).
-template <typename... KArgs, typename... Args>
-lbq_status launch_overlapped(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, dim3 cluster, cudaStream_t st,
-                             Args... args) {
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return LBQ_ECUDA;
+// before it wrote).  The kernel's shared memory limit is raised to the device's
+// once per device; setting it again, from another thread too, changes nothing.
+template <auto Kern, typename... Args>
+lbq_status launch_overlapped(dim3 grid, int threads, size_t smem, dim3 cluster, cudaStream_t st, const Args&... args) {
+    if (smem > 48 * 1024) {
+        static std::atomic<uint64_t> raised{0};
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return LBQ_ECUDA;
+        const uint64_t bit = uint64_t(1) << (dev & 63);
+        if (dev > 63 || !(raised.load(std::memory_order_relaxed) & bit)) {
+            // what the kernel's own shared memory leaves of the 227 KB
+            cudaFuncAttributes fa;
+            if (cudaFuncGetAttributes(&fa, Kern) != cudaSuccess ||
+                cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     227 * 1024 - static_cast<int>(fa.sharedSizeBytes)) != cudaSuccess) {
+                (void)cudaGetLastError();
+                return LBQ_ECUDA;
+            }
+            raised.fetch_or(bit, std::memory_order_relaxed);
+        }
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -30,11 +42,11 @@ lbq_status launch_overlapped(void (*kern)(KArgs...), dim3 grid, int threads, siz
         attr[1].val.clusterDim.z = cluster.z;
         cfg.numAttrs = 2;
     }
-    if (cudaLaunchKernelEx(&cfg, kern, KArgs(args)...) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, Kern, args...) != cudaSuccess) {
         (void)cudaGetLastError();
         return LBQ_ECUDA;
     }
-    return last_launch();
+    return LBQ_OK;
 }
 
 lbq_status check_i8weight(const lbq_i8weight* q, bool need_data) {
@@ -54,17 +66,25 @@ template <int SRC, bool SCALED, bool BESIDE>
 lbq_status run_i8_quantize(const void* in, int64_t rows, int64_t len, const float* chan, int8_t* codes, int64_t ldc,
                            float* scale, cudaStream_t st) {
     const int64_t nvec = len / 8;
-    auto go = [&](auto kern, int threads) {
-        return launch_overlapped(kern, dim3(static_cast<unsigned>(rows)), threads, 0, dim3(1, 1, 1), st, in, len, chan,
-                                 codes, ldc, scale);
-    };
+    const dim3 grid(static_cast<unsigned>(rows)), one(1, 1, 1);
     // the fewest threads that hold the row in registers, up to 64 bytes each
-    if (nvec <= 256) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 1, 256>, 256);
-    if (nvec <= 512) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 2, 256>, 256);
-    if (nvec <= 1024) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 256>, 256);
-    if (nvec <= 2048) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 512>, 512);
-    if (nvec <= 4096) return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 1024>, 1024);
-    return go(i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 0, 1024>, 1024);
+    if (nvec <= 256)
+        return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 1, 256>>(grid, 256, 0, one, st, in, len, chan,
+                                                                                       codes, ldc, scale);
+    if (nvec <= 512)
+        return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 2, 256>>(grid, 256, 0, one, st, in, len, chan,
+                                                                                       codes, ldc, scale);
+    if (nvec <= 1024)
+        return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 256>>(grid, 256, 0, one, st, in, len, chan,
+                                                                                       codes, ldc, scale);
+    if (nvec <= 2048)
+        return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 512>>(grid, 512, 0, one, st, in, len, chan,
+                                                                                       codes, ldc, scale);
+    if (nvec <= 4096)
+        return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 1024>>(grid, 1024, 0, one, st, in, len,
+                                                                                        chan, codes, ldc, scale);
+    return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 0, 1024>>(grid, 1024, 0, one, st, in, len, chan,
+                                                                                    codes, ldc, scale);
 }
 
 template <bool COL, int MT, int R8>
@@ -73,10 +93,10 @@ lbq_status launch_i8_adapter(const void* in, int64_t m, int64_t len, const void*
     // parts enough for two CTAs per SM
     const int64_t groups = cdiv(m, MT), chunks = cdiv(len, kAdChunk);
     const int64_t parts = std::min<int64_t>({kAdMaxParts, chunks, std::max<int64_t>(1, 2 * sms / groups)});
-    return launch_overlapped(i8_adapter_kernel<COL, MT, R8>, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts)),
-                             kAdThreads, AdapterSmem<MT, R8>::kBytes, dim3(1, static_cast<unsigned>(parts), 1), st,
-                             static_cast<const uint16_t*>(in), m, static_cast<int>(len), static_cast<const uint16_t*>(wt), r,
-                             out);
+    return launch_overlapped<i8_adapter_kernel<COL, MT, R8>>(
+        dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts)), kAdThreads, AdapterSmem<MT, R8>::kBytes,
+        dim3(1, static_cast<unsigned>(parts), 1), st, static_cast<const uint16_t*>(in), m, static_cast<int>(len),
+        static_cast<const uint16_t*>(wt), r, out);
 }
 
 template <bool COL, int NR>
@@ -94,9 +114,9 @@ lbq_status launch_i8_adapter_tc(const void* in, int64_t m, int64_t len, const vo
     if (!ok) return LBQ_ECUDA;
     const int64_t groups = cdiv(m, 128), blocks = cdiv(len, 64);
     const int64_t parts = std::min<int64_t>({kAdMaxParts, blocks, std::max<int64_t>(1, sms / groups)});
-    return launch_overlapped(i8_adapter_tc_kernel<COL, NR>, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts)),
-                             kAdTcThreads, AdapterTcSmem<NR>::kBytes, dim3(1, static_cast<unsigned>(parts), 1), st, tmX, tmW,
-                             static_cast<int>(m), static_cast<int>(len), r, out);
+    return launch_overlapped<i8_adapter_tc_kernel<COL, NR>>(
+        dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts)), kAdTcThreads, AdapterTcSmem<NR>::kBytes,
+        dim3(1, static_cast<unsigned>(parts), 1), st, tmX, tmW, static_cast<int>(m), static_cast<int>(len), r, out);
 }
 
 template <bool COL>
@@ -116,31 +136,13 @@ lbq_status run_i8_adapter(const void* in, int64_t m, int64_t len, const void* wt
     return launch_i8_adapter<COL, MT, 8>(in, m, len, wt, r, out, sms, st);
 }
 
-// Codes and scales of the tokens and, with an adapter, its product `out`.
+// The adapter's product of the tokens.
 template <bool BWD>
-lbq_status run_i8_tokens(const void* in, int64_t m, int64_t len, const float* chan, const void* wt, int r, int8_t* codes,
-                         int64_t ldc, float* scale, float* out, int sms, cudaStream_t st) {
-    if (r == 0) return run_i8_quantize<kSrcBf16, BWD, false>(in, m, len, chan, codes, ldc, scale, st);
-    const lbq_status s = m <= 16                 ? run_i8_adapter<BWD, 16>(in, m, len, wt, r, out, sms, st)
-                         : !BWD || r % 8 == 0 ? run_i8_adapter_tc<BWD>(in, m, len, wt, r, out, sms, st)
-                                              : run_i8_adapter<BWD, 64>(in, m, len, wt, r, out, sms, st);
-    if (s != LBQ_OK) return s;
-    return run_i8_quantize<kSrcBf16, BWD, true>(in, m, len, chan, codes, ldc, scale, st);
-}
-
-// Codes and scales of the tokens in a call's workspace.
-struct I8Tokens {
-    int64_t ld;          // bytes of a code row, a multiple of 16
-    size_t scale_at;     // offset of the scales
-    size_t bytes;
-};
-
-I8Tokens i8_tokens(int m, int64_t len) {
-    I8Tokens t;
-    t.ld = static_cast<int64_t>(round_up(static_cast<size_t>(len), 16));
-    t.scale_at = round_up(static_cast<size_t>(m) * static_cast<size_t>(t.ld), 256);
-    t.bytes = t.scale_at + round_up(static_cast<size_t>(m) * sizeof(float), 256);
-    return t;
+lbq_status run_i8_factor(const void* in, int64_t m, int64_t len, const void* wt, int r, float* out, int sms,
+                         cudaStream_t st) {
+    if (m <= 16) return run_i8_adapter<BWD, 16>(in, m, len, wt, r, out, sms, st);
+    if (!BWD || r % 8 == 0) return run_i8_adapter_tc<BWD>(in, m, len, wt, r, out, sms, st);
+    return run_i8_adapter<BWD, 64>(in, m, len, wt, r, out, sms, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -159,74 +161,133 @@ bool make_map_i8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t col
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct I8Job {
-    const lbq_i8weight* w;
-    const int8_t* codes;   // tokens
-    int64_t ld;
-    I8Params p;
-};
-
-template <int NT, bool TRANS, int RP>
-lbq_status launch_i8_split(const I8Job& j, int nsplit, cudaStream_t st) {
-    CUtensorMap tmW, tmX;
-    if (!make_map_i8(&tmW, j.w->codes, j.w->n, j.w->k, j.w->k, 128) ||
-        !make_map_i8(&tmX, j.codes, j.p.m, j.p.red, j.ld, NT))
-        return LBQ_ECUDA;
-    const dim3 grid(static_cast<unsigned>(cdiv(j.p.out, 128)), static_cast<unsigned>(cdiv(j.p.m, NT)),
-                    static_cast<unsigned>(nsplit));
-    return launch_overlapped(i8_split_kernel<NT, TRANS, RP>, grid, kI8SplitThreads, I8SplitCfg<NT>::kBytes,
-                             dim3(1, 1, static_cast<unsigned>(nsplit)), st, tmW, tmX, j.p);
-}
-
-template <int NT, bool TRANS, int RP>
-lbq_status launch_i8_pair(const I8Job& j, int sms, cudaStream_t st) {
-    CUtensorMap tmW, tmX;
-    if (!make_map_i8(&tmW, j.w->codes, j.w->n, j.w->k, j.w->k, 128) ||
-        !make_map_i8(&tmX, j.codes, j.p.m, j.p.red, j.ld, NT / 2))
-        return LBQ_ECUDA;
-    const int64_t tiles = cdiv(j.p.out, 256) * cdiv(j.p.m, NT);
-    const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles, std::max(1, sms / 2)));
-    return launch_overlapped(i8_pair_kernel<NT, TRANS, RP>, dim3(2 * pairs), kI8PairThreads, (I8PairCfg<NT, RP>::kBytes),
-                             dim3(2, 1, 1), st, tmW, tmX, j.p);
-}
-
+// The plan of one call's product: CTA pairs on 256 x 256 tiles when these fill
+// the machine, else split CTAs on token tiles of nt, with the reduction in
+// nsplit parts.
 struct I8Plan {
-    int nt;        // tokens of a tile
-    bool pair;     // CTA pairs, else split CTAs
-    int nsplit;    // parts of the reduction (split CTAs)
+    bool pair;
+    I8SplitShape sh;             // split CTAs
+    int nsplit;
 };
 
 I8Plan plan_i8(int m, int64_t out, int64_t red, int sms) {
     I8Plan pl{};
-    pl.nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
-    pl.nsplit = 1;
-    if (m > 128 && cdiv(out, 256) * cdiv(m, 256) >= sms / 2) {
+    const int64_t blocks = cdiv(red, 128);
+    if (m > 128 && cdiv(out, kI8Tile) * cdiv(m, kI8Tile) >= sms / 2) {
         pl.pair = true;
-        pl.nt = 256;
         return pl;
     }
-    const int64_t tiles = cdiv(out, 128) * cdiv(m, pl.nt), blocks = cdiv(red, 128);
-    const int64_t want = std::max<int64_t>(1, 2 * sms / tiles);
+    const int64_t ttiles = cdiv(m, 256);
+    pl.sh.nt = static_cast<int>(round_up(static_cast<size_t>(cdiv(m, ttiles)), 16));
+    // two CTAs per SM while their rings hold three blocks each
+    const int per_sm = pl.sh.nt <= 128 ? 2 : 1;
+    const int64_t want = std::max<int64_t>(1, per_sm * sms / (cdiv(out, 128) * ttiles));
     pl.nsplit = static_cast<int>(std::min<int64_t>({want, kI8MaxSplit, std::max<int64_t>(1, blocks / 4)}));
+    pl.sh.tok = static_cast<int>(cdiv(pl.sh.nt, pl.nsplit));
     return pl;
 }
 
-template <bool TRANS, int RP>
-lbq_status run_i8_product_rp(const I8Job& j, int sms, cudaStream_t st) {
-    const I8Plan pl = plan_i8(j.p.m, j.p.out, j.p.red, sms);
-    if (pl.pair) return launch_i8_pair<256, TRANS, RP>(j, sms, st);
-    if (cdiv(j.p.m, pl.nt) > 65535) return LBQ_EUNSUPPORTED;
-    switch (pl.nt) {
-        case 16: return launch_i8_split<16, TRANS, RP>(j, pl.nsplit, st);
-        case 32: return launch_i8_split<32, TRANS, RP>(j, pl.nsplit, st);
-        case 64: return launch_i8_split<64, TRANS, RP>(j, pl.nsplit, st);
-        default: return launch_i8_split<128, TRANS, RP>(j, pl.nsplit, st);
-    }
+// The ring of a split CTA: as many blocks as its share of the SM's shared
+// memory holds beside the factors of its tokens (rank rounded to rp), at least 2.
+I8SplitShape split_shape(const I8Plan& pl, int64_t red, int rp) {
+    I8SplitShape sh = pl.sh;
+    const int64_t budget = (sh.nt <= 128 ? 106 : 210) * 1024 - int64_t(sh.tok) * rp * 4 - sh.nt * 4;
+    const int64_t blocks = std::max<int64_t>(2, cdiv(cdiv(red, 128), pl.nsplit));
+    sh.stages = static_cast<int>(std::min<int64_t>({kI8SplitMaxStages, blocks, std::max<int64_t>(2, budget / sh.stage_bytes())}));
+    return sh;
 }
 
+// Codes and scales of the tokens in a call's workspace.
+struct I8Space {
+    int64_t ld;          // bytes of a code row, a multiple of 16
+    size_t scale_at, bytes;
+};
+
+I8Space i8_space(int m, int64_t red) {
+    I8Space t;
+    t.ld = static_cast<int64_t>(round_up(static_cast<size_t>(red), 16));
+    t.scale_at = round_up(static_cast<size_t>(m) * static_cast<size_t>(t.ld), 256);
+    t.bytes = t.scale_at + round_up(static_cast<size_t>(m) * sizeof(float), 256);
+    return t;
+}
+
+struct I8Job {
+    const lbq_i8weight* w;
+    const void* tokens;    // bf16 [m, red]
+    const float* chan;     // their channel scales (backward)
+    const void* factor;    // the adapter's factor that multiplies the tokens
+    float* saved;          // their product
+    int8_t* codes;         // of the tokens, in the workspace
+    float* scale;
+    int64_t ld;
+    I8Params p;
+};
+
+template <bool TRANS, int RP>
+lbq_status launch_i8_split(const I8Job& j, const I8Plan& pl, cudaStream_t st) {
+    CUtensorMap tmW, tmX;
+    if (!make_map_i8(&tmW, j.w->codes, j.w->n, j.w->k, j.w->k, 128) ||
+        !make_map_i8(&tmX, j.codes, j.p.m, j.p.red, j.ld, pl.sh.nt))
+        return LBQ_ECUDA;
+    const I8SplitShape sh = split_shape(pl, j.p.red, RP);
+    const dim3 grid(static_cast<unsigned>(cdiv(j.p.out, 128)), static_cast<unsigned>(cdiv(j.p.m, sh.nt)),
+                    static_cast<unsigned>(pl.nsplit));
+    return launch_overlapped<i8_split_kernel<TRANS, RP>>(grid, kI8SplitThreads, sh.bytes(RP),
+                                                         dim3(1, 1, static_cast<unsigned>(pl.nsplit)), st, tmW, tmX, j.p, sh);
+}
+
+template <bool TRANS, int RP>
+lbq_status launch_i8_pair(const I8Job& j, int sms, cudaStream_t st) {
+    CUtensorMap tmW, tmX;
+    if (!make_map_i8(&tmW, j.w->codes, j.w->n, j.w->k, j.w->k, 128) ||
+        !make_map_i8(&tmX, j.codes, j.p.m, j.p.red, j.ld, 128))
+        return LBQ_ECUDA;
+    const int64_t tiles = cdiv(j.p.out, kI8Tile) * cdiv(j.p.m, kI8Tile);
+    const unsigned pairs = static_cast<unsigned>(std::min<int64_t>(tiles, std::max(1, sms / 2)));
+    return launch_overlapped<i8_pair_kernel<TRANS, RP>>(dim3(2 * pairs), kI8PairThreads, I8PairCfg<RP>::kBytes,
+                                                        dim3(2, 1, 1), st, tmW, tmX, j.p);
+}
+
+// The adapter's product, the tokens' codes, the product.
+template <bool TRANS, int RP>
+lbq_status run_i8_product(const I8Job& j, const I8Plan& pl, int sms, cudaStream_t st) {
+    lbq_status s = LBQ_OK;
+    if (RP > 0) s = run_i8_factor<TRANS>(j.tokens, j.p.m, j.p.red, j.factor, j.p.rank, j.saved, sms, st);
+    if (s == LBQ_OK)
+        s = run_i8_quantize<kSrcBf16, TRANS, (RP > 0)>(j.tokens, j.p.m, j.p.red, j.chan, j.codes, j.ld, j.scale, st);
+    if (s != LBQ_OK) return s;
+    return pl.pair ? launch_i8_pair<TRANS, RP>(j, sms, st) : launch_i8_split<TRANS, RP>(j, pl, st);
+}
+
+// One call: forward (TRANS false, in = X) or input gradient (in = dY).  A and B
+// are the adapter's factors, saved its product with the tokens.
 template <bool TRANS>
-lbq_status run_i8_product(const I8Job& j, int sms, cudaStream_t st) {
-    if (j.p.rank == 0) return run_i8_product_rp<TRANS, 0>(j, sms, st);
-    if (j.p.rank <= 16) return run_i8_product_rp<TRANS, 16>(j, sms, st);
-    return run_i8_product_rp<TRANS, 64>(j, sms, st);
+lbq_status run_i8_linear(const void* in, int m, const lbq_i8weight* q, const void* A, const void* B, int rank, float s,
+                         float* out, float* saved, void* ws, const I8Space& at, int sms, cudaStream_t st) {
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    I8Job j{};
+    j.w = q;
+    j.tokens = in;
+    j.chan = TRANS ? q->scale : nullptr;
+    j.factor = TRANS ? B : A;
+    j.saved = saved;
+    j.codes = reinterpret_cast<int8_t*>(w);
+    j.scale = reinterpret_cast<float*>(w + at.scale_at);
+    j.ld = at.ld;
+    j.p.m = m;
+    j.p.out = TRANS ? q->k : q->n;
+    j.p.red = TRANS ? q->n : q->k;
+    j.p.row_scale = j.scale;
+    j.p.out_scale = TRANS ? nullptr : q->scale;
+    j.p.rank = rank;
+    j.p.s = s;
+    j.p.T = saved;
+    j.p.P = static_cast<const uint16_t*>(TRANS ? A : B);
+    j.p.pj = TRANS ? 1 : rank;
+    j.p.pu = TRANS ? q->k : 1;
+    j.p.Y = out;
+    const I8Plan pl = plan_i8(m, j.p.out, j.p.red, sms);
+    if (rank == 0) return run_i8_product<TRANS, 0>(j, pl, sms, st);
+    if (rank <= 16) return run_i8_product<TRANS, 16>(j, pl, sms, st);
+    return run_i8_product<TRANS, 64>(j, pl, sms, st);
 }

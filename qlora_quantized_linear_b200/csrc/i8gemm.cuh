@@ -19,6 +19,8 @@
 #pragma once
 
 #include "common.cuh"
+#include "dqgemm.cuh"
+#include "dqgemm_bwd.cuh"
 
 namespace lbq {
 
@@ -69,83 +71,44 @@ __device__ __forceinline__ uint64_t i8_a_desc(uint32_t tile, int j) {
                  : smem_desc_k_sw128(tile) + static_cast<uint64_t>(2 * j);
 }
 
-// Adapter factors of one output feature, zero beyond the rank.
-template <int RP>
-__device__ __forceinline__ void i8_load_factor(const I8Params& p, int64_t j, bool ok, float (&b)[RP > 0 ? RP : 1]) {
-    if (RP > 0) {
-#pragma unroll
-        for (int u = 0; u < RP; ++u)
-            b[u] = (ok && u < p.rank) ? bf16_bits_to_f32(__ldg(p.P + j * p.pj + u * p.pu)) : 0.0f;
-    }
-}
-
-// sum_u T[t, u] b[u]; `row` is the same for all lanes of the warp.
-template <int RP>
-__device__ __forceinline__ float i8_factor_dot(const float* row, int rank, const float (&b)[RP > 0 ? RP : 1]) {
-    float d = 0.0f;
-    if ((rank & 3) == 0) {
-#pragma unroll
-        for (int u = 0; u < RP; u += 4) {
-            if (u < rank) {
-                const float4 t = __ldg(reinterpret_cast<const float4*>(row + u));
-                d = fmaf(t.x, b[u], d);
-                d = fmaf(t.y, b[u + 1], d);
-                d = fmaf(t.z, b[u + 2], d);
-                d = fmaf(t.w, b[u + 3], d);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int u = 0; u < RP; ++u)
-            if (u < rank) d = fmaf(__ldg(row + u), b[u], d);
-    }
-    return d;
-}
-
-// Y of one output feature j for N consecutive tokens from t.
-template <int RP, int N>
-__device__ __forceinline__ void i8_store(const I8Params& p, int t, int64_t j, const int (&acc)[N], float so,
-                                         const float (&b)[RP > 0 ? RP : 1]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (t + i < p.m) {
-            float v = static_cast<float>(acc[i]) * __ldg(p.row_scale + t + i) * so;
-            if (RP > 0) v = fmaf(p.s, i8_factor_dot<RP>(p.T + static_cast<int64_t>(t + i) * p.rank, p.rank, b), v);
-            p.Y[static_cast<int64_t>(t + i) * p.out + j] = v;
-        }
-    }
-}
-
 // ---------------------------------------------------------------------------
-// Few tokens: one CTA per 128 output features x NT tokens x part of the
+// Few tokens: one CTA per 128 output features x nt tokens x part of the
 // reduction.  The CTAs of a cluster hold the parts of one tile; each adds up
-// its share of the tokens over the cluster's shared memory.
+// its share of the tokens over the cluster's shared memory.  nt is any multiple
+// of 16 up to 256, so that a ragged batch multiplies few empty tokens.
+// HBM-bound by the weight; the ring's blocks (16 KB of weight and nt x 128
+// bytes of tokens) in flight cover the latency.
 // ---------------------------------------------------------------------------
 constexpr int kI8SplitThreads = 192;      // producer warp, MMA warp, four epilogue warps
 constexpr int kI8MaxSplit = 8;
+constexpr int kI8SplitMaxStages = 12;
 
-template <int NT>
-struct I8SplitCfg {
-    static constexpr int kStages = NT <= 16 ? 6 : NT <= 32 ? 5 : NT <= 64 ? 4 : 3;   // two CTAs per SM
-    static constexpr int kABytes = 128 * 128;
-    static constexpr int kBBytes = NT * 128;
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr size_t kBar = size_t(kStages) * kStageBytes;
-    static constexpr size_t kBytes = kBar + (2 * kStages + 1) * 8 + 16 + 1024;
-    static_assert(size_t(NT) * 512 <= kBar, "the partial sums reuse the ring");
+// Shared memory of a CTA: the ring (the partial sums reuse it), the token
+// scales, s T of the CTA's share of the tokens, the barriers.
+struct I8SplitShape {
+    int nt, stages, tok;
+    __host__ __device__ int stage_bytes() const { return 128 * 128 + nt * 128; }
+    __host__ __device__ int ring() const {
+        const int sums = (nt * 512 + 1023) / 1024 * 1024;
+        return stages * stage_bytes() > sums ? stages * stage_bytes() : sums;
+    }
+    __host__ __device__ size_t bytes(int rp) const {
+        return static_cast<size_t>(ring()) + nt * 4 + static_cast<size_t>(tok) * rp * 4 + (2 * stages + 1) * 8 + 16 + 1024;
+    }
 };
 
-template <int NT, bool TRANS, int RP>
+template <bool TRANS, int RP>
 __global__ void __launch_bounds__(kI8SplitThreads)
     i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                    const __grid_constant__ I8Params p) {
-    using C = I8SplitCfg<NT>;
-    constexpr int S = C::kStages;
-    constexpr uint32_t kTmemCols = NT < 32 ? 32 : NT;
-    constexpr uint32_t kIdesc = idesc_i8_s32(128, NT, TRANS);
+                    const __grid_constant__ I8Params p, const I8SplitShape sh) {
+    const int NT = sh.nt, S = sh.stages, stage_bytes = sh.stage_bytes();
+    const uint32_t kTmemCols = tmem_cols_for(NT);
+    const uint32_t kIdesc = idesc_i8_s32(128, NT, TRANS);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBar);
+    float* sx = reinterpret_cast<float*>(smem + sh.ring());
+    float* sT = sx + NT;                                     // [tok][RP]
+    uint64_t* full = reinterpret_cast<uint64_t*>(sT + sh.tok * RP);
     uint64_t* empty = full + S;
     uint64_t* dfull = empty + S;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(dfull + 1);
@@ -179,112 +142,159 @@ __global__ void __launch_bounds__(kI8SplitThreads)
 
     if (warp == 0) {
         if (lane == 0) {
-            auto load_w = [&](int i) {
-                uint8_t* a = smem + (i % S) * C::kStageBytes;
-                mbar_arrive_expect_tx(&full[i % S], C::kStageBytes);
-                if (TRANS) tma_load_2d(a, &tmW, &full[i % S], j0, (b0 + i) * 128);
-                else tma_load_2d(a, &tmW, &full[i % S], (b0 + i) * 128, j0);
+            auto load_w = [&](int i, int st) {
+                uint8_t* a = smem + st * stage_bytes;
+                mbar_arrive_expect_tx(&full[st], stage_bytes);
+                if (TRANS) tma_load_2d(a, &tmW, &full[st], j0, (b0 + i) * 128);
+                else tma_load_2d(a, &tmW, &full[st], (b0 + i) * 128, j0);
             };
             // the weight does not depend on the kernel before this one (which
             // starts only after everything before it is complete), the codes
             // of the tokens do
             const int ahead = nb < S ? nb : S;
-            for (int i = 0; i < ahead; ++i) load_w(i);
+            for (int i = 0; i < ahead; ++i) load_w(i, i);
             griddep_wait();
             griddep_launch_dependents();
-            int i = 0;
+            int i = 0, st = 0;
+            uint32_t ph = 1;                                 // the first pass over the ring does not wait
             for (; i < nb; ++i) {
                 if (i >= S) {
-                    if (!mbar_wait(&empty[i % S], ((i / S) - 1) & 1, s_abort)) break;
-                    load_w(i);
+                    if (!mbar_wait(&empty[st], ph, s_abort)) break;
+                    load_w(i, st);
                 }
-                tma_load_2d(smem + (i % S) * C::kStageBytes + C::kABytes, &tmX, &full[i % S], (b0 + i) * 128, t0);
+                tma_load_2d(smem + st * stage_bytes + 128 * 128, &tmX, &full[st], (b0 + i) * 128, t0);
+                if (++st == S) st = 0, ph ^= 1u;
             }
             for (int d = max(0, i - S); d < i; ++d) mbar_wait_drain(&full[d % S], (d / S) & 1);
         }
     } else if (warp == 1) {
         if (lane == 0) {
+            int st = 0;
+            uint32_t ph = 0;
             for (int i = 0; i < nb; ++i) {
-                if (!mbar_wait(&full[i % S], (i / S) & 1, s_abort)) break;
+                if (!mbar_wait(&full[st], ph, s_abort)) break;
                 tc_fence_after();
-                const uint32_t a = smem_u32(smem + (i % S) * C::kStageBytes);
-                const uint64_t bdesc = smem_desc_k_sw128(a + C::kABytes);
+                const uint32_t a = smem_u32(smem + st * stage_bytes);
+                const uint64_t bdesc = smem_desc_k_sw128(a + 128 * 128);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     mma_i8_ss(tmem, i8_a_desc<TRANS>(a, j), bdesc + static_cast<uint64_t>(2 * j), kIdesc,
                               (i > 0 || j > 0) ? 1u : 0u);
-                mma_commit(&empty[i % S]);
+                mma_commit(&empty[st]);
+                if (++st == S) st = 0, ph ^= 1u;
             }
             mma_commit(dfull);
             mbar_wait_drain(dfull, 0);
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        griddep_wait();
-        const int quarter = warp & 3;
-        const int64_t j = j0 + quarter * 32 + lane;
+        const int tid = threadIdx.x - 64, quarter = warp & 3;
+        const int live = min(NT, p.m - t0);                  // tokens of this tile
+        const int lo = live * part / nsplit, hi = live * (part + 1) / nsplit;   // this CTA's share of them
+        // this thread's output feature, its scale and adapter factors
+        const int f = quarter * 32 + lane;
+        const int64_t j = j0 + f;
         const bool ok = j < p.out;
+        griddep_wait();
+        for (int t = tid; t < live; t += 128) sx[t] = __ldg(p.row_scale + t0 + t);
+        if (RP > 0)
+            for (int e = tid; e < (hi - lo) * RP; e += 128) {
+                const int t = e / RP, u = e - t * RP;
+                sT[e] = u < p.rank ? p.s * __ldg(p.T + static_cast<int64_t>(t0 + lo + t) * p.rank + u) : 0.0f;
+            }
+        const float so = (ok && p.out_scale) ? __ldg(p.out_scale + j) : 1.0f;
+        float b[RP > 0 ? RP : 1];
+        if (RP > 0) {
+#pragma unroll
+            for (int u = 0; u < RP; ++u)
+                b[u] = (ok && u < p.rank) ? bf16_bits_to_f32(__ldg(p.P + j * p.pj + u * p.pu)) : 0.0f;
+        }
+        named_barrier_sync(1, 128);
+        // consecutive tokens from t (of this CTA's share) with their sums
+        auto store = [&](int t, auto& acc, int n) {
+            float* y = p.Y + static_cast<int64_t>(t0 + t) * p.out + j;
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(sizeof(acc) / sizeof(int)); ++i) {
+                if (i < n) {
+                    float v = static_cast<float>(acc[i]) * sx[t + i] * so;
+                    if (RP > 0) {
+                        float d = 0.0f;
+                        const float4* tr = reinterpret_cast<const float4*>(sT + (t - lo + i) * RP);
+#pragma unroll
+                        for (int u = 0; u < RP; u += 4) {
+                            if (u < p.rank) {
+                                const float4 x = tr[u / 4];
+                                d = fmaf(x.x, b[u], d);
+                                d = fmaf(x.y, b[u + 1], d);
+                                d = fmaf(x.z, b[u + 2], d);
+                                d = fmaf(x.w, b[u + 3], d);
+                            }
+                        }
+                        v += d;
+                    }
+                    if (ok) *y = v;
+                    y += p.out;
+                }
+            }
+        };
         const bool done = mbar_wait(dfull, 0, s_abort);
         tc_fence_after();
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         if (nsplit == 1) {
-            float b[RP > 0 ? RP : 1];
-            i8_load_factor<RP>(p, j, ok, b);
-            const float so = (ok && p.out_scale) ? __ldg(p.out_scale + j) : 1.0f;
 #pragma unroll 1
-            for (int c = 0; done && c < NT && t0 + c < p.m; c += 16) {
+            for (int c = 0; done && c < live; c += 16) {
                 uint32_t r[16];
                 tmem_ld_32x32b_x16(taddr + c, r);
                 tmem_ld_wait();
                 int acc[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[i] = static_cast<int>(r[i]);
-                if (ok) i8_store<RP, 16>(p, t0 + c, j, acc, so, b);
+                store(c, acc, live - c);
+                __syncwarp();
             }
-        } else if (done) {
+        } else {
             // this part's sums to shared memory: [token][feature]
             int* buf = reinterpret_cast<int*>(smem);
 #pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
+            for (int c = 0; done && c < live; c += 16) {
                 uint32_t r[16];
                 tmem_ld_32x32b_x16(taddr + c, r);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) buf[(c + i) * 128 + quarter * 32 + lane] = static_cast<int>(r[i]);
+                for (int i = 0; i < 16; ++i) buf[(c + i) * 128 + f] = static_cast<int>(r[i]);
             }
-        }
-    }
-    tc_fence_before();
-    if (nsplit > 1) {
-        __syncwarp();
-        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-        if (warp >= 2) {
-            const int f = (warp - 2) * 32 + lane;
-            const int64_t j = j0 + f;
-            const bool ok = j < p.out;
-            float b[RP > 0 ? RP : 1];
-            i8_load_factor<RP>(p, j, ok, b);
-            const float so = (ok && p.out_scale) ? __ldg(p.out_scale + j) : 1.0f;
-            const int live = min(NT, p.m - t0);              // tokens of this tile
-            const int c1 = live * (part + 1) / nsplit;
+            tc_fence_before();
+            __syncwarp();
+            asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
             const uint32_t base = smem_u32(smem) + f * 4;
-            for (int c = live * part / nsplit; c < c1; ++c) {
-                int sum = 0;
+#pragma unroll 1
+            for (int c = lo; c < hi; c += 4) {
+                int acc[4] = {0, 0, 0, 0};
 #pragma unroll
                 for (int r = 0; r < kI8MaxSplit; ++r) {
                     if (r < nsplit) {
                         uint32_t remote;
-                        int x;
                         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(base + c * 512), "r"(r));
-                        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(remote) : "memory");
-                        sum += x;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (c + i < hi) {
+                                int x;
+                                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(remote + i * 512) : "memory");
+                                acc[i] += x;
+                            }
+                        }
                     }
                 }
-                const int acc[1] = {sum};
-                if (ok) i8_store<RP, 1>(p, t0 + c, j, acc, so, b);
+                store(c, acc, hi - c);
             }
         }
-        __syncwarp();
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (nsplit > 1) {
+        // the producer and MMA warps meet the epilogue's first cluster barrier here
+        if (warp < 2)
+            asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
         // every CTA's shared memory stays until all have read it
         asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     } else {
@@ -297,80 +307,44 @@ __global__ void __launch_bounds__(kI8SplitThreads)
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: a pair of CTAs computes 256 output features x NT tokens with
+// Many tokens: a pair of CTAs computes 256 output features x 256 tokens with
 // tcgen05.mma.cta_group::2.  Each CTA loads its 128 features of the weight and
 // its half of the tokens; the pair's tensor cores share the token halves, so
 // an SM reads and stages half the token bytes per MMA that it would alone.
-// The kernel is persistent (one pair per two SMs) with two accumulators in
+// Loads alone and MMAs alone each take nearly as long as both together, so
+// shared memory and L2 are left to them: the adapter's term is not formed from
+// shared memory by the epilogue (that took 49 us of a 219 us forward of 4096
+// tokens x 14336 x 4096 at rank 16) but by the tensor cores too, in fp32.  s T is
+// split there into three bf16 parts that add up to it exactly (8 + 8 + 8 bits),
+// so the term is as exact as in fp32.
+//
+// The kernel is persistent (one pair per two SMs), with two accumulators in
 // tensor memory: eight epilogue warps drain one while the MMAs fill the other.
+// With an adapter the epilogue first takes the int32 sums to registers; the
+// term's MMAs then write fp32 over them, issued between two blocks of the next
+// tile, so that the tensor cores never wait for the epilogue.
+// Dealing out the last waves' tiles in equal parts of their reduction was
+// measured too: 3% less time for a reduction of 14336, 3 to 8% more for 4096.
 // ---------------------------------------------------------------------------
 constexpr int kI8PairThreads = 320;       // producer warp, MMA warp, eight epilogue warps
+constexpr int kI8Tile = 256;              // output features and tokens of a pair's tile
 
-// RP: the adapter's rank rounded up to 0, 16 or 64; its factors of a tile are
-// staged in shared memory (T as fp32 [NT][RP + 4], the other factor as bf16
-// [128][RP + 4]: rows that the epilogue's reads meet without bank conflicts).
-template <int NT, int RP>
+// RP: the adapter's rank rounded up to 0, 16 or 64.  Its operands are K-major
+// tiles of 128-byte rows (128-byte swizzle): P [128 features][rank], and s T
+// [128 tokens] with the three parts side by side (RP 16) or in tiles of their
+// own (RP 64).
+template <int RP>
 struct I8PairCfg {
-    static constexpr int kStages = RP > 16 ? 4 : 6;
-    static constexpr int kABytes = 128 * 128;
-    static constexpr int kBBytes = NT / 2 * 128;
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kRow = RP + 4;
-    static constexpr size_t kScale = size_t(kStages) * kStageBytes;          // token scales, fp32 [NT]
-    static constexpr size_t kT = kScale + size_t(NT) * 4;
-    static constexpr size_t kP = kT + (RP > 0 ? size_t(NT) * kRow * 4 : 0);
-    static constexpr size_t kBar = kP + (RP > 0 ? size_t(128) * kRow * 2 : 0);
-    static constexpr size_t kBytes = kBar + (2 * kStages + 4) * 8 + 16 + 1024;
+    static constexpr int kStages = RP > 16 ? 5 : 6;
+    static constexpr int kOperand = 128 * 128;                               // also an adapter tile
+    static constexpr int kStageBytes = 2 * kOperand;
+    static constexpr size_t kP = size_t(kStages) * kStageBytes;
+    static constexpr size_t kT = kP + (RP > 0 ? kOperand : 0);
+    static constexpr size_t kScale = kT + (RP > 16 ? 3 : RP > 0 ? 1 : 0) * kOperand;   // token scales, fp32 [8 warps][128]
+    static constexpr size_t kBar = kScale + (RP > 0 ? 0 : 4096);
+    static constexpr size_t kBytes = kBar + (2 * kStages + 6) * 8 + 16 + 1024;
     static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
-
-// 16 lanes x 32 columns of 32 bits, 16 registers: lane (g, c) gets rows g
-// (registers 4 i, 4 i + 1) and g + 8 (4 i + 2, 4 i + 3) at columns 8 i + 2 c
-// and 8 i + 2 c + 1.
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-
-// The staged factors of a tile: s T (zero beyond the tokens and the rank) and
-// the other factor of this CTA's 128 output features, by 256 threads.
-template <int NT, int RP>
-__device__ __forceinline__ void i8_stage_factors(const I8Params& p, int64_t j0, int t0, float* sT, uint16_t* sP, int tid) {
-    constexpr int ROW = RP + 4;
-    const int ru = (p.rank + 3) / 4 * 4;
-    if ((p.rank & 3) == 0) {
-        const int q = ru / 4;
-        for (int e = tid; e < NT * q; e += 256) {
-            const int t = e / q, u = (e - t * q) * 4;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (t0 + t < p.m) v = __ldg(reinterpret_cast<const float4*>(p.T + static_cast<int64_t>(t0 + t) * p.rank + u));
-            v.x *= p.s, v.y *= p.s, v.z *= p.s, v.w *= p.s;
-            *reinterpret_cast<float4*>(sT + t * ROW + u) = v;
-        }
-    } else {
-        for (int e = tid; e < NT * ru; e += 256) {
-            const int t = e / ru, u = e - t * ru;
-            sT[t * ROW + u] =
-                (t0 + t < p.m && u < p.rank) ? p.s * __ldg(p.T + static_cast<int64_t>(t0 + t) * p.rank + u) : 0.0f;
-        }
-    }
-    if (p.pj == 1) {                         // the features are contiguous: neighbours to neighbouring threads
-        for (int e = tid; e < 128 * ru; e += 256) {
-            const int u = e >> 7, f = e & 127;
-            sP[f * ROW + u] = (j0 + f < p.out && u < p.rank) ? __ldg(p.P + j0 + f + u * p.pu) : uint16_t(0);
-        }
-    } else {                                 // the ranks are
-        for (int e = tid; e < 128 * ru; e += 256) {
-            const int f = e / ru, u = e - f * ru;
-            sP[f * ROW + u] = (j0 + f < p.out && u < p.rank) ? __ldg(p.P + (j0 + f) * p.pj + u) : uint16_t(0);
-        }
-    }
-}
 
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t smem_addr, uint32_t rank) {
     uint32_t r;
@@ -402,6 +376,43 @@ __device__ __forceinline__ void mma_i8_ss_pair(uint32_t d_tmem, uint64_t a_desc,
         : "memory");
 }
 
+__device__ __forceinline__ void mma_bf16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// mbar_wait for arrivals from the other CTA of the pair too: acquires at cluster
+// scope.  (A separate fence.acq_rel.cluster after the wait cost the MMA issuer
+// 1.5 us a tile.)
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    auto test = [&](uint32_t sleep_ns) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(sleep_ns)
+            : "memory");
+        return ok != 0;
+    };
+    if (test(0u)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 0; it < kWaitLimitIters; ++it) {
+        if (test(20000u)) return true;
+        if (*abort) return false;
+        if ((it & 63u) == 63u && globaltimer_ns() - t0 > kWaitLimitNs) break;
+    }
+    *abort = 1;
+    record_status(kStatusTimeout);
+    return false;
+}
+
 // Arrive on the barrier at this offset in both CTAs of the pair.
 __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
     asm volatile(
@@ -409,26 +420,107 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
         ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
 }
 
-template <int NT, bool TRANS, int RP>
+__device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// The two halves of a register pair's top bf16 parts, and what is left of them:
+// truncated, so that three of them hold an fp32 value exactly.  An infinity or
+// a NaN leaves nothing.
+__device__ __forceinline__ uint32_t i8_split_part(float& a, float& b) {
+    const uint32_t ua = __float_as_uint(a) & 0xFFFF0000u, ub = __float_as_uint(b) & 0xFFFF0000u;
+    const uint32_t w = (ua >> 16) | ub;
+    a = (ua & 0x7F800000u) == 0x7F800000u ? 0.0f : a - __uint_as_float(ua);
+    b = (ub & 0x7F800000u) == 0x7F800000u ? 0.0f : b - __uint_as_float(ub);
+    return w;
+}
+
+// The adapter operands of a tile for this CTA: P of 128 features from j0, s T of
+// 128 tokens from t0 (zero beyond the sizes and the rank), by 256 threads.
+template <int RP>
+__device__ __forceinline__ void i8_stage_factors(const I8Params& p, int64_t j0, int t0, uint8_t* sP, uint8_t* sT, int tid) {
+    constexpr int UNITS = RP / 8;                       // 16-byte units of a row
+    for (int e = tid; e < 128 * UNITS; e += 256) {
+        const int t = e / UNITS, un = e % UNITS, u0 = un * 8;
+        float v[8];
+        const float* row = p.T + static_cast<int64_t>(t0 + t) * p.rank + u0;
+        if (t0 + t < p.m && (p.rank & 3) == 0) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (u0 + 4 * q < p.rank) x = __ldg(reinterpret_cast<const float4*>(row + 4 * q));
+                v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = (t0 + t < p.m && u0 + u < p.rank) ? __ldg(row + u) : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] *= p.s;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+            uint4 w;
+            w.x = i8_split_part(v[0], v[1]);
+            w.y = i8_split_part(v[2], v[3]);
+            w.z = i8_split_part(v[4], v[5]);
+            w.w = i8_split_part(v[6], v[7]);
+            const int unit = RP <= 16 ? part * 2 + un : un;
+            *reinterpret_cast<uint4*>(sT + (RP <= 16 ? 0 : part * 16384) + t * 128 + ((unit ^ (t & 7)) << 4)) = w;
+        }
+    }
+    for (int e = tid; e < 128 * UNITS; e += 256) {
+        // neighbouring threads take what is contiguous: the features (backward) or the ranks
+        const int f = p.pj == 1 ? e & 127 : e / UNITS, un = p.pj == 1 ? e >> 7 : e % UNITS;
+        const int64_t j = j0 + f;
+        const uint16_t* src = p.P + j * p.pj;
+        uint4 w;
+        if (p.pj != 1 && (p.rank & 7) == 0) {
+            w = make_uint4(0u, 0u, 0u, 0u);
+            if (j < p.out && un * 8 < p.rank) w = __ldg(reinterpret_cast<const uint4*>(src + un * 8));
+        } else {
+            uint32_t h[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                h[u] = (j < p.out && un * 8 + u < p.rank) ? __ldg(src + (un * 8 + u) * p.pu) : 0u;
+            w = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+        }
+        *reinterpret_cast<uint4*>(sP + f * 128 + ((un ^ (f & 7)) << 4)) = w;
+    }
+}
+
+template <bool TRANS, int RP>
 __global__ void __launch_bounds__(kI8PairThreads, 1)
     i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                    const __grid_constant__ I8Params p) {
-    using C = I8PairCfg<NT, RP>;
+    using C = I8PairCfg<RP>;
     constexpr int S = C::kStages;
-    constexpr uint32_t kTmemCols = 2 * NT;
-    constexpr uint32_t kIdesc = idesc_i8_s32(256, NT, TRANS);
+    constexpr uint32_t kIdesc = idesc_i8_s32(256, kI8Tile, TRANS), kIdescF = idesc_bf16_f32(256, kI8Tile);
+    constexpr int kTermBlock = 5;           // the term of a tile follows this block of the next one
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sP = smem + C::kP;
+    uint8_t* sT = smem + C::kT;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBar);   // used in the first CTA of the pair
     uint64_t* empty = full + S;                                     // both
-    uint64_t* dfull = empty + S;                                    // both, one per accumulator
-    uint64_t* dempty = dfull + 2;                                   // first CTA
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(dempty + 2);
+    uint64_t* dfull = empty + S;                                    // both: sums of a buffer complete
+    uint64_t* dempty = dfull + 2;                                   // first CTA: buffer drained
+    uint64_t* tready = dempty + 2;                                  // first CTA: term's operands staged, sums taken
+    uint64_t* tfull = tready + 1;                                   // both: term complete
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tfull + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = blockIdx.x & 1u;
-    const int jtiles = (p.out + 255) / 256;
-    const int tiles = jtiles * ((p.m + NT - 1) / NT);
+    const int jtiles = (p.out + kI8Tile - 1) / kI8Tile;
+    const int tiles = jtiles * ((p.m + kI8Tile - 1) / kI8Tile);
     const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
     const int nb = (p.red + 127) / 128;
 
@@ -441,6 +533,8 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
             mbar_init(&dfull[i], 1);
             mbar_init(&dempty[i], 16);       // eight epilogue warps of each CTA
         }
+        mbar_init(tready, 16);
+        mbar_init(tfull, 1);
         *s_abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmW);
@@ -448,7 +542,7 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(smem_u32(s_tmem)), "r"(kTmemCols) : "memory");
+                     ::"r"(smem_u32(s_tmem)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
@@ -466,7 +560,7 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
                 uint8_t* a = smem + st * C::kStageBytes;
                 if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * C::kStageBytes);
                 const uint32_t bar = map_to_rank(smem_u32(&full[st]), 0);
-                const int j0 = (tile % jtiles) * 256 + static_cast<int>(rank) * 128;
+                const int j0 = (tile % jtiles) * kI8Tile + static_cast<int>(rank) * 128;
                 if (TRANS) tma_load_2d_pair(a, &tmW, bar, j0, b * 128);
                 else tma_load_2d_pair(a, &tmW, bar, b * 128, j0);
             };
@@ -477,7 +571,7 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
             griddep_launch_dependents();
             bool ok = true;
             for (int tile = first; ok && tile < tiles; tile += step) {
-                const int t0 = (tile / jtiles) * NT + static_cast<int>(rank) * (NT / 2);
+                const int t0 = (tile / jtiles) * kI8Tile + static_cast<int>(rank) * 128;
                 for (int b = 0; b < nb; ++b, ++it) {
                     const int st = it % S;
                     if (it >= ahead) {
@@ -487,8 +581,8 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
                         }
                         load_w(it, tile, b);
                     }
-                    tma_load_2d_pair(smem + st * C::kStageBytes + C::kABytes, &tmX,
-                                     map_to_rank(smem_u32(&full[st]), 0), b * 128, t0);
+                    tma_load_2d_pair(smem + st * C::kStageBytes + C::kOperand, &tmX, map_to_rank(smem_u32(&full[st]), 0),
+                                     b * 128, t0);
                 }
             }
             // the last slots are released: no copy is in flight and no commit is
@@ -502,148 +596,128 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
         if (lane == 0 && rank == 0) {
             int it = 0, n = 0;
             bool ok = true;
+            // the adapter's term of the pair's n-th tile
+            auto term = [&](int i) {
+                if (!mbar_wait_cluster(tready, i & 1, s_abort)) return false;
+                tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>((i & 1) * kI8Tile);
+                const uint64_t pd = smem_desc_k_sw128(smem_u32(sP));
+                for (int part = 0; part < 3; ++part) {
+                    const uint64_t td = smem_desc_k_sw128(smem_u32(sT) + (RP <= 16 ? part * 32 : part * 16384));
+                    for (int k = 0; k * 16 < p.rank; ++k)
+                        mma_bf16_ss_pair(d, pd + static_cast<uint64_t>(2 * k), td + static_cast<uint64_t>(2 * k), kIdescF,
+                                         (part > 0 || k > 0) ? 1u : 0u);
+                }
+                mma_commit_pair(tfull);
+                return true;
+            };
             for (int tile = first; ok && tile < tiles; tile += step, ++n) {
                 const int buf = n & 1;
-                ok = n < 2 || mbar_wait(&dempty[buf], ((n >> 1) - 1) & 1, s_abort);
+                ok = n < 2 || mbar_wait_cluster(&dempty[buf], ((n >> 1) - 1) & 1, s_abort);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(buf * NT);
+                const uint32_t d = tmem + static_cast<uint32_t>(buf * kI8Tile);
                 for (int b = 0; b < nb; ++b, ++it) {
                     const int st = it % S;
                     ok = mbar_wait(&full[st], (it / S) & 1, s_abort);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t a = smem_u32(smem + st * C::kStageBytes);
-                    const uint64_t bdesc = smem_desc_k_sw128(a + C::kABytes);
+                    const uint64_t bdesc = smem_desc_k_sw128(a + C::kOperand);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         mma_i8_ss_pair(d, i8_a_desc<TRANS>(a, j), bdesc + static_cast<uint64_t>(2 * j), kIdesc,
                                        (b > 0 || j > 0) ? 1u : 0u);
                     mma_commit_pair(&empty[st]);
+                    if (RP > 0 && n > 0 && b == min(kTermBlock, nb - 1)) {
+                        ok = term(n - 1);
+                        if (!ok) break;
+                    }
                 }
                 if (ok) mma_commit_pair(&dfull[buf]);
             }
+            if (RP > 0 && ok && n > 0) ok = term(n - 1);
             // given up: the MMAs issued so far end before tensor memory is freed
             if (!ok && it > 0) mbar_wait_drain(&empty[(it - 1) % S], ((it - 1) / S) & 1);
         }
     } else {
         // ------------------------------------------------------------ epilogue
+        // lane = output feature: 128 contiguous bytes of Y per token; a warp takes
+        // 32 features and half of the tokens
         griddep_wait();
         const int quarter = warp & 3, half = (warp - 2) >> 2, tid = threadIdx.x - 64;
-        float* sx = reinterpret_cast<float*>(smem + C::kScale);
-        float* sT = reinterpret_cast<float*>(smem + C::kT);
-        uint16_t* sP = reinterpret_cast<uint16_t*>(smem + C::kP);
+        float* sx = reinterpret_cast<float*>(smem + C::kScale) + (warp - 2) * 128;   // the warp's copy (no adapter)
+        auto arrive = [&](uint64_t* bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(bar), 0));
+        };
         int n = 0;
         for (int tile = first; tile < tiles; tile += step, ++n) {
             const int buf = n & 1;
-            const int64_t j0 = static_cast<int64_t>(tile % jtiles) * 256 + static_cast<int>(rank) * 128;
-            const int t0 = (tile / jtiles) * NT, h0 = half * (NT / 2);
-            // the tile's scales and factors, while its MMAs run
-            named_barrier_sync(1, 256);
-            if (tid < NT) sx[tid] = t0 + tid < p.m ? __ldg(p.row_scale + t0 + tid) : 0.0f;
-            if (RP > 0) i8_stage_factors<NT, RP>(p, j0, t0, sT, sP, tid);
-            named_barrier_sync(1, 256);
-            const uint32_t taddr = tmem + static_cast<uint32_t>(buf * NT + h0) + (static_cast<uint32_t>(quarter * 32) << 16);
-            const int live = min(NT / 2, p.m - t0 - h0);          // tokens of this warp's half that exist
-            float* y = p.Y + static_cast<int64_t>(t0 + h0) * p.out + j0 + quarter * 32;
-            if (RP == 0) {
-                // lane = output feature: 128 contiguous bytes per token
-                const int64_t j = j0 + quarter * 32 + lane;
-                const bool ok = j < p.out;
-                const float so = (ok && p.out_scale) ? __ldg(p.out_scale + j) : 1.0f;
-                if (!mbar_wait(&dfull[buf], (n >> 1) & 1, s_abort)) continue;   // given up: still meet at the barriers
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < NT / 2; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld_32x32b_x16(taddr + c, r);
-                    tmem_ld_wait();
-                    if (c + 16 >= NT / 2) {
-                        // the last columns are in registers: the accumulator is free
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&dempty[buf]), 0));
-                    }
-                    float* row = y + static_cast<int64_t>(c) * p.out + lane;
+            // the term's operands, while the sums are still being formed (the last tile's term,
+            // which read the same shared memory, is complete: the warp has waited for it)
+            if (RP > 0) {
+                i8_stage_factors<(RP > 0 ? RP : 16)>(
+                    p, static_cast<int64_t>(tile % jtiles) * kI8Tile + static_cast<int>(rank) * 128,
+                    (tile / jtiles) * kI8Tile + static_cast<int>(rank) * 128, sP, sT, tid);
+                fence_proxy_async_smem();
+            }
+            const int64_t j = static_cast<int64_t>(tile % jtiles) * kI8Tile + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+            const int t0 = (tile / jtiles) * kI8Tile + half * 128;
+            const int live = min(128, p.m - t0);              // tokens of this warp's half that exist
+            const bool ok = j < p.out;
+            const float so = (ok && p.out_scale) ? __ldg(p.out_scale + j) : 1.0f;
+            float sv[4];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (ok && c + i < live) *row = static_cast<float>(static_cast<int>(r[i])) * sx[h0 + c + i] * so;
+            for (int q = 0; q < 4; ++q) sv[q] = q * 32 + lane < live ? __ldg(p.row_scale + t0 + q * 32 + lane) : 0.0f;
+            float* row = p.Y + static_cast<int64_t>(t0) * p.out + j;
+            const uint32_t taddr = tmem + static_cast<uint32_t>(buf * kI8Tile + half * 128) + (static_cast<uint32_t>(quarter * 32) << 16);
+            if (!mbar_wait(&dfull[buf], (n >> 1) & 1, s_abort)) break;
+            tc_fence_after();
+            if (RP == 0) {
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sx[q * 32 + lane] = sv[q];
+                __syncwarp();
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(taddr + c, r);
+                    tmem_ld_wait();
+                    if (c == 96) arrive(&dempty[buf]);        // the last columns are in registers
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (ok && c + i < live) *row = static_cast<float>(static_cast<int>(r[i])) * sx[c + i] * so;
                         row += p.out;
                     }
                     __syncwarp();
                 }
             } else {
-                // lane (g, c): four features 8 apart, two tokens of every eight, so that a
-                // value read from shared memory serves several outputs
-                const int g = lane >> 2, c2 = (lane & 3) * 2;
-                const int ru = (p.rank + 3) / 4 * 4;
-                float so[4];
-                bool ok[4];
+                uint32_t r[4][32];
 #pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    const int64_t j = j0 + quarter * 32 + 8 * f + g;
-                    ok[f] = j < p.out;
-                    so[f] = (ok[f] && p.out_scale) ? __ldg(p.out_scale + j) : 1.0f;
-                }
-                if (!mbar_wait(&dfull[buf], (n >> 1) & 1, s_abort)) continue;   // given up: still meet at the barriers
+                for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(taddr + 32 * q, r[q]);
+                tmem_ld_wait();
+                arrive(tready);
+                // scaled while the term's MMAs run
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        r[q][i] = __float_as_uint(static_cast<float>(static_cast<int>(r[q][i])) *
+                                                  __shfl_sync(0xFFFFFFFFu, sv[q], i) * so);
+                if (!mbar_wait(tfull, n & 1, s_abort)) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < NT / 2; c += 32) {
-                    uint32_t r[2][16];
-                    tmem_ld_16x256b_x4(taddr + c, r[0]);
-                    tmem_ld_16x256b_x4(taddr + c + (16u << 16), r[1]);
-                    float d[4][4][2];                               // [feature][token group][token]
 #pragma unroll
-                    for (int f = 0; f < 4; ++f)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) d[f][i][0] = d[f][i][1] = 0.0f;
-                    const float* tr = sT + (h0 + c + c2) * C::kRow;
-                    const uint16_t* pr = sP + (quarter * 32 + g) * C::kRow;
-#pragma unroll 1
-                    for (int u = 0; u < ru; u += 4) {
-                        float b[4][4];
-#pragma unroll
-                        for (int f = 0; f < 4; ++f) {
-                            const uint2 w = *reinterpret_cast<const uint2*>(pr + 8 * f * C::kRow + u);
-                            b[f][0] = __uint_as_float(w.x << 16);
-                            b[f][1] = __uint_as_float(w.x & 0xFFFF0000u);
-                            b[f][2] = __uint_as_float(w.y << 16);
-                            b[f][3] = __uint_as_float(w.y & 0xFFFF0000u);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const float4 t = *reinterpret_cast<const float4*>(tr + (8 * i + k) * C::kRow + u);
-#pragma unroll
-                                for (int f = 0; f < 4; ++f) {
-                                    d[f][i][k] = fmaf(t.x, b[f][0], d[f][i][k]);
-                                    d[f][i][k] = fmaf(t.y, b[f][1], d[f][i][k]);
-                                    d[f][i][k] = fmaf(t.z, b[f][2], d[f][i][k]);
-                                    d[f][i][k] = fmaf(t.w, b[f][3], d[f][i][k]);
-                                }
-                            }
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t d[32];
+                    tmem_ld_32x32b_x32(taddr + 32 * q, d);
                     tmem_ld_wait();
-                    if (c + 32 >= NT / 2) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&dempty[buf]), 0));
-                    }
+                    if (q == 3) arrive(&dempty[buf]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 sxv = *reinterpret_cast<const float2*>(sx + h0 + c + 8 * i + c2);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int t = c + 8 * i + c2 + k;
-                            float* row = y + static_cast<int64_t>(t) * p.out + g;
-#pragma unroll
-                            for (int f = 0; f < 4; ++f) {
-                                const int acc = static_cast<int>(r[f >> 1][4 * i + 2 * (f & 1) + k]);
-                                const float v = static_cast<float>(acc) * (k ? sxv.y : sxv.x) * so[f];
-                                if (ok[f] && t < live) row[8 * f] = v + d[f][i][k];
-                            }
-                        }
+                    for (int i = 0; i < 32; ++i) {
+                        if (ok && 32 * q + i < live) *row = __uint_as_float(r[q][i]) + __uint_as_float(d[i]);
+                        row += p.out;
                     }
                     __syncwarp();
                 }
@@ -656,7 +730,7 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 

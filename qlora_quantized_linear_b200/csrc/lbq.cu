@@ -2,6 +2,7 @@
 // tile and split selection, and kernel launches.  One translation unit holds
 // every kernel so that the device status word is a single object.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -1142,12 +1143,12 @@ lbq_status lbq_quantize_i8(const void* X, int dtype, int rows, int k, int8_t* co
 
 size_t lbq_linear_i8_fwd_workspace_size(int m, const lbq_i8weight* q, int rank) {
     if (m < 1 || rank < 0 || rank > kLoraMaxRank || check_i8weight(q, false) != LBQ_OK) return 0;
-    return i8_tokens(m, q->k).bytes;
+    return i8_space(m, q->k).bytes;
 }
 
 size_t lbq_linear_i8_bwd_workspace_size(int m, const lbq_i8weight* q, int rank) {
     if (m < 1 || rank < 0 || rank > kLoraMaxRank || check_i8weight(q, false) != LBQ_OK) return 0;
-    return i8_tokens(m, q->n).bytes;
+    return i8_space(m, q->n).bytes;
 }
 
 lbq_status lbq_linear_i8_fwd(const void* X, int m, const lbq_i8weight* q, const void* A, const void* B, int rank,
@@ -1158,29 +1159,11 @@ lbq_status lbq_linear_i8_fwd(const void* X, int m, const lbq_i8weight* q, const 
     if (m < 1 || !X || !Y) return LBQ_EINVAL;
     if (!aligned16(X) || !aligned16(Y)) return LBQ_EALIGN;
     if ((st = check_lora(rank, A, B, T_save)) != LBQ_OK) return st;
-    const I8Tokens tok = i8_tokens(m, q->k);
-    if (!workspace || workspace_bytes < tok.bytes) return LBQ_EWORKSPACE;
+    const I8Space at = i8_space(m, q->k);
+    if (!workspace || workspace_bytes < at.bytes) return LBQ_EWORKSPACE;
     if (!aligned16(workspace)) return LBQ_EALIGN;
-    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    int8_t* codes = static_cast<int8_t*>(workspace);
-    float* scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tok.scale_at);
-    const int sms = sm_count();
-    if ((st = run_i8_tokens<false>(X, m, q->k, nullptr, A, rank, codes, tok.ld, scale, T_save, sms, cs)) != LBQ_OK)
-        return st;
-    I8Job j{q, codes, tok.ld, {}};
-    j.p.m = m;
-    j.p.out = q->n;
-    j.p.red = q->k;
-    j.p.row_scale = scale;
-    j.p.out_scale = q->scale;
-    j.p.rank = rank;
-    j.p.s = s;
-    j.p.T = T_save;
-    j.p.P = static_cast<const uint16_t*>(B);
-    j.p.pj = rank;
-    j.p.pu = 1;
-    j.p.Y = Y;
-    return run_i8_product<false>(j, sms, cs);
+    return run_i8_linear<false>(X, m, q, A, B, rank, s, Y, T_save, workspace, at, sm_count(),
+                                reinterpret_cast<cudaStream_t>(stream));
 }
 
 lbq_status lbq_linear_i8_bwd(const void* dY, int m, const lbq_i8weight* q, const void* A, const void* B, int rank,
@@ -1191,29 +1174,11 @@ lbq_status lbq_linear_i8_bwd(const void* dY, int m, const lbq_i8weight* q, const
     if (m < 1 || !dY || !dX || q->n % 8 != 0 || q->n > kI8MaxReduction) return LBQ_EINVAL;
     if (!aligned16(dY) || !aligned16(dX)) return LBQ_EALIGN;
     if ((st = check_lora(rank, A, B, U_save)) != LBQ_OK) return st;
-    const I8Tokens tok = i8_tokens(m, q->n);
-    if (!workspace || workspace_bytes < tok.bytes) return LBQ_EWORKSPACE;
+    const I8Space at = i8_space(m, q->n);
+    if (!workspace || workspace_bytes < at.bytes) return LBQ_EWORKSPACE;
     if (!aligned16(workspace)) return LBQ_EALIGN;
-    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    int8_t* codes = static_cast<int8_t*>(workspace);
-    float* scale = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tok.scale_at);
-    const int sms = sm_count();
-    if ((st = run_i8_tokens<true>(dY, m, q->n, q->scale, B, rank, codes, tok.ld, scale, U_save, sms, cs)) != LBQ_OK)
-        return st;
-    I8Job j{q, codes, tok.ld, {}};
-    j.p.m = m;
-    j.p.out = q->k;
-    j.p.red = q->n;
-    j.p.row_scale = scale;
-    j.p.out_scale = nullptr;
-    j.p.rank = rank;
-    j.p.s = s;
-    j.p.T = U_save;
-    j.p.P = static_cast<const uint16_t*>(A);
-    j.p.pj = 1;
-    j.p.pu = q->k;
-    j.p.Y = dX;
-    return run_i8_product<true>(j, sms, cs);
+    return run_i8_linear<true>(dY, m, q, A, B, rank, s, dX, U_save, workspace, at, sm_count(),
+                               reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t lbq_grad_norm_workspace_size(int count) { return count < 1 ? 0 : clip_workspace(count); }

@@ -550,8 +550,9 @@ class Int8Weight:
             scale = torch.empty(n, dtype=torch.float32, device=device)
         self.codes = _out(codes, (self.n, self.k), torch.int8, "codes", codes)
         self.scale = _out(scale, (self.n,), torch.float32, "scale", scale)
-        if self.codes.device != self.scale.device:
-            raise ValueError("codes and scale must be on one device")
+        if self.codes.device != self.scale.device or not self.codes.is_cuda:
+            raise ValueError("codes and scale must be on one CUDA device")
+        self.device_index = self.codes.get_device()
         self.struct = lbq_i8weight(n=self.n, k=self.k, codes=self.codes.data_ptr(), scale=self.scale.data_ptr())
         self._ref = ctypes.byref(self.struct)
 
@@ -578,27 +579,52 @@ def linear_i8_bwd_workspace(m: int, qw: Int8Weight, rank: int = 0):
     return torch.empty(lbq_linear_i8_bwd_workspace_size(m, qw._ref, rank), dtype=torch.uint8, device=qw.codes.device)
 
 
+def _f32_out(t, m, n, name, like):
+    """An fp32 [m, n] output of the caller, checked, or a new one."""
+    torch = _torch()
+    if t is None:
+        return torch.empty((m, n), dtype=torch.float32, device=like.device)
+    if t.dtype is not torch.float32 or t.shape != (m, n) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {(m, n)}")
+    return t
+
+
 def _linear_i8(call, what, space, x, name, width_in, width_out, qw, A, B, s, out, out_name, saved, saved_name,
                workspace, stream):
     torch = _torch()
-    x = _bf16_2d(x, name)
-    m = x.shape[0]
-    if x.shape[1] != width_in:
+    dev, bf16 = qw.device_index, torch.bfloat16
+    if x.dtype is not bf16 or x.dim() != 2 or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 2-D bf16 CUDA tensor")
+    m, width = x.shape
+    if width != width_in:
         raise ValueError(f"{name} must have {width_in} columns")
-    if (A is None) != (B is None):
-        raise ValueError("A and B come together")
+    out = _f32_out(out, m, width_out, out_name, x)
+    a = b = t = None
     rank = 0
-    if A is not None:
-        A, B, rank = _bf16_2d(A, "A"), _bf16_2d(B, "B"), A.shape[0]
-        if A.shape[1] != qw.k or tuple(B.shape) != (qw.n, rank):
-            raise ValueError(f"A must be [rank, {qw.k}] and B [{qw.n}, rank]")
-    out = _out(out, (m, width_out), torch.float32, out_name, x)
-    saved = _out(saved, (m, rank), torch.float32, saved_name, x) if rank else None
+    if A is None and B is None:
+        saved = None
+    elif A is None or B is None:
+        raise ValueError("A and B come together")
+    else:
+        rank = A.shape[0]
+        if A.dtype is not bf16 or B.dtype is not bf16 or A.shape != (rank, qw.k) or B.shape != (qw.n, rank) or \
+                not A.is_contiguous() or not B.is_contiguous():
+            raise ValueError(f"A must be contiguous bf16 [rank, {qw.k}] and B [{qw.n}, rank]")
+        saved = _f32_out(saved, m, rank, saved_name, x)
+        if A.get_device() != dev or B.get_device() != dev or saved.get_device() != dev:
+            raise ValueError(f"A, B and {saved_name} must be on the weight's device")
+        a, b, t = A.data_ptr(), B.data_ptr(), saved.data_ptr()
     if workspace is None:
         workspace = space(m, qw, rank)
-    _same_device(x.device, codes=qw.codes, A=A, B=B, workspace=workspace, **{out_name: out, saved_name: saved})
-    _check(call(x.data_ptr(), m, qw._ref, _ptr(A), _ptr(B), rank, float(s), out.data_ptr(), _ptr(saved),
-                workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)), what)
+    if x.get_device() != dev or out.get_device() != dev or workspace.get_device() != dev:
+        raise ValueError(f"{name}, {out_name} and the workspace must be on the weight's device")
+    # the library launches on the current device
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{dev}, not on the current CUDA device")
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    rc = call(x.data_ptr(), m, qw._ref, a, b, rank, s, out.data_ptr(), t, workspace.data_ptr(), workspace.nbytes, st)
+    if rc != LBQ_OK:
+        raise LbqError(rc, what)
     return out, saved
 
 
@@ -656,10 +682,13 @@ class GradClip:
 
     def clip(self, max_norm: float, stream=None):
         """Scale the gradients by min(1, max_norm / (norm + 1e-6)); returns their norm before."""
-        _same_device(self.total_norm.device)
-        _check(lbq_clip_grad_norm(self.table, len(self.grads), float(max_norm), self.total_norm.data_ptr(),
-                                  self.workspace.data_ptr(), self.workspace.numel(), _stream(stream)),
-               "lbq_clip_grad_norm")
+        torch = _torch()
+        dev = self.total_norm.get_device()
+        if dev != torch._C._cuda_getDevice():
+            raise ValueError(f"the gradients are on cuda:{dev}, not on the current CUDA device")
+        st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+        _check(lbq_clip_grad_norm(self.table, len(self.grads), max_norm, self.total_norm.data_ptr(),
+                                  self.workspace.data_ptr(), self.workspace.nbytes, st), "lbq_clip_grad_norm")
         return self.total_norm
 
 

@@ -178,6 +178,8 @@ SIZES = [
     (513, 2000, 640, 16),
     # enough tiles for the paired kernel, ragged in both directions
     (2600, 2000, 160, 0), (2600, 2000, 160, 7), (2305, 2561, 1168, 16), (2305, 2568, 400, 64),
+    # several waves of tiles, the last ones shared between pairs
+    (4200, 4208, 272, 0), (4110, 4368, 528, 16),
 ]
 
 
