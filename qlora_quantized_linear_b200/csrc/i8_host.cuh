@@ -64,27 +64,30 @@ lbq_status check_i8weight(const lbq_i8weight* q, bool need_data) {
 // ---------------------------------------------------------------------------
 template <int SRC, bool SCALED, bool BESIDE>
 lbq_status run_i8_quantize(const void* in, int64_t rows, int64_t len, const float* chan, int8_t* codes, int64_t ldc,
-                           float* scale, cudaStream_t st) {
+                           float* scale, int sms, cudaStream_t st) {
+#define LBQ_I8_ROWS(NV, THREADS)                                                                                       \
+    launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, NV, THREADS>>(                                      \
+        dim3(static_cast<unsigned>(rows)), THREADS, 0, dim3(1, 1, 1), st, in, len, chan, codes, ldc, scale)
     const int64_t nvec = len / 8;
-    const dim3 grid(static_cast<unsigned>(rows)), one(1, 1, 1);
-    // the fewest threads that hold the row in registers, up to 64 bytes each
-    if (nvec <= 256)
-        return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 1, 256>>(grid, 256, 0, one, st, in, len, chan,
-                                                                                       codes, ldc, scale);
-    if (nvec <= 512)
-        return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 2, 256>>(grid, 256, 0, one, st, in, len, chan,
-                                                                                       codes, ldc, scale);
-    if (nvec <= 1024)
-        return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 256>>(grid, 256, 0, one, st, in, len, chan,
-                                                                                       codes, ldc, scale);
-    if (nvec <= 2048)
-        return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 512>>(grid, 512, 0, one, st, in, len, chan,
-                                                                                       codes, ldc, scale);
-    if (nvec <= 4096)
-        return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 4, 1024>>(grid, 1024, 0, one, st, in, len,
-                                                                                        chan, codes, ldc, scale);
-    return launch_overlapped<i8_quantize_rows_kernel<SRC, SCALED, BESIDE, 0, 1024>>(grid, 1024, 0, one, st, in, len, chan,
-                                                                                    codes, ldc, scale);
+    if (SRC == kSrcBf16 && rows < 2 * sms) {
+        // few rows: latency, so a piece or two per thread
+        if (nvec <= 256) return LBQ_I8_ROWS(1, 256);
+        if (nvec <= 512) return LBQ_I8_ROWS(1, 512);
+        if (nvec <= 1024) return LBQ_I8_ROWS(1, 1024);
+        if (nvec <= 2048) return LBQ_I8_ROWS(2, 1024);
+    } else {
+        // many rows: fewer threads with more pieces each (4096 x 4096: 10 us with 128
+        // threads, 16 with 512; 4096 x 14336: 28 with 256, 32 with 512, 40 with 1024)
+        if (nvec <= 256) return LBQ_I8_ROWS(2, 128);
+        if (nvec <= 512) return LBQ_I8_ROWS(4, 128);
+        if (nvec <= 1024) return LBQ_I8_ROWS(4, 256);
+        if (nvec <= 1792) return LBQ_I8_ROWS(7, 256);
+        if (nvec <= 2048) return LBQ_I8_ROWS(4, 512);
+        if (nvec <= 3584) return LBQ_I8_ROWS(7, 512);
+    }
+    if (nvec <= 4096) return LBQ_I8_ROWS(4, 1024);
+    return LBQ_I8_ROWS(0, 1024);
+#undef LBQ_I8_ROWS
 }
 
 template <bool COL, int MT, int R8>
@@ -254,7 +257,7 @@ lbq_status run_i8_product(const I8Job& j, const I8Plan& pl, int sms, cudaStream_
     lbq_status s = LBQ_OK;
     if (RP > 0) s = run_i8_factor<TRANS>(j.tokens, j.p.m, j.p.red, j.factor, j.p.rank, j.saved, sms, st);
     if (s == LBQ_OK)
-        s = run_i8_quantize<kSrcBf16, TRANS, (RP > 0)>(j.tokens, j.p.m, j.p.red, j.chan, j.codes, j.ld, j.scale, st);
+        s = run_i8_quantize<kSrcBf16, TRANS, (RP > 0)>(j.tokens, j.p.m, j.p.red, j.chan, j.codes, j.ld, j.scale, sms, st);
     if (s != LBQ_OK) return s;
     return pl.pair ? launch_i8_pair<TRANS, RP>(j, sms, st) : launch_i8_split<TRANS, RP>(j, pl, st);
 }

@@ -208,9 +208,13 @@ __global__ void __launch_bounds__(kAdThreads) i8_adapter_kernel(const uint16_t* 
 // ---------------------------------------------------------------------------
 constexpr int kAdTcThreads = 192;          // producer warp, MMA warp, four epilogue warps
 
+// The ring takes over half of the SM's shared memory: one CTA per SM.  With two
+// or three, the CTAs that start early, while the product of the call before is
+// still busy on the other SMs, crowd the first free ones, and the kernel lasted
+// 49 instead of 28 us behind a 4096-token product (117 MB of tokens).
 template <int NR>
 struct AdapterTcSmem {
-    static constexpr int kStages = 4;
+    static constexpr int kStages = NR <= 16 ? 7 : NR <= 32 ? 6 : 5;
     static constexpr int kXBytes = 128 * 128;
     static constexpr int kWBytes = NR * 128;
     static constexpr int kStageBytes = kXBytes + kWBytes;

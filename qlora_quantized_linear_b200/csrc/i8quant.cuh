@@ -6,12 +6,19 @@
 //
 // The codes are those of the exact quotient, so they do not depend on how a
 // reciprocal rounds; bf16 data meets exact ties often (v = amax / 2 is 63.5).
-// The fast path multiplies by inv = fp32(127 / amax), 2^-24 relative off: for
-// |v inv| <= 127 the exact product lies within 2^-17 of the quotient, and the
-// rounded value is right unless it lies within 2^-16 of a half-integer.  Those
-// elements are compared exactly: in fp32 where the values are short (ties are
-// common in bf16), else 127 v with the half-integer times amax in fp64, where
-// both products are exact (24 + 8 bits).
+// The codes come from v inv with inv = 127 / amax rounded up, at most 2^-23
+// relative above it: for |v inv| <= 127 the exact product lies within 2^-16 of
+// the quotient, and its rounding is right unless it lies that close to a
+// half-integer.
+//   bf16: a quotient of two 8-bit numbers that is no half-integer is farther
+//   away than that (2^-16 relative), so only exact ties are left.  They need
+//   127 to divide mantissa(amax) (2 k + 1): either the tie is 63.5, which goes
+//   up to the even 64 as inv does, or the mantissa is 254 and inv a power of
+//   two, so that the product is exact.  Nothing has to be looked at.
+//   fp16 has more such mantissas (127 c for c = 9 .. 16), fp32 any quotient:
+//   there a value within 2^-15 of a half-integer (one in 2^14) has 127 v
+//   compared with the half-integer times amax in fp64, where both products are
+//   exact (24 + 8 bits).
 //
 // HBM-bound: a row is read once and stays in registers between its maximum and
 // its codes.
@@ -27,7 +34,7 @@ enum I8Src : int { kSrcF32 = LBQ_F32, kSrcBf16 = LBQ_BF16, kSrcF16 = LBQ_F16 };
 
 struct I8RowScale {
     float f;      // power of two applied to the values first (rows of very small or large values)
-    float inv;    // fp32(127 / (amax f)); 0 for a row without codes
+    float inv;    // 127 / (amax f), rounded up; 0 for a row without codes
     float a;      // amax f
     float scale;  // the stored scale
 };
@@ -44,7 +51,7 @@ __device__ __forceinline__ I8RowScale i8_row_scale(uint32_t amax_bits) {
         // brought near 1 first (exact for every value that has a code but 0)
         r.f = a < 0x1p-60f ? 0x1p100f : a > 0x1p60f ? 0x1p-100f : 1.0f;
         r.a = a * r.f;
-        r.inv = __fdiv_rn(127.0f, r.a);
+        r.inv = __fdiv_ru(127.0f, r.a);
         r.scale = __fdiv_rn(a, 127.0f);
     }
     return r;
@@ -97,13 +104,11 @@ __device__ __forceinline__ float absmax3(float m, float a, float b) {
 }
 
 // The codes of eight values, first in the low byte.  v inv + 1.5 * 2^23 in one
-// fma leaves the rounded integer in the low bits of the sum; the distance of
-// v inv from it, again one fma, tells whether any of the eight is close enough
-// to a half-integer to be looked at exactly.  SHORT: the values have at most
-// 11 significant bits (bf16, fp16); there exact ties are common, and
-// e = 127 v - q a is exact in one fma (both products have at most 18 bits, and
-// near a half-integer v is at least a / 254), so that 2 |e| against a decides.
-template <bool SHORT>
+// fma leaves the rounded integer in the low bits of the sum.  EXACT: the
+// distance of v inv from it, again one fma, tells whether any of the eight is
+// close enough to a half-integer to be looked at exactly; bf16 values need no
+// look.
+template <bool EXACT>
 __device__ __forceinline__ uint2 i8_codes8(f32x2 (&v)[4], const I8RowScale& r) {
     if (r.inv == 0.0f) return make_uint2(0u, 0u);
     if (r.f != 1.0f) {
@@ -113,37 +118,28 @@ __device__ __forceinline__ uint2 i8_codes8(f32x2 (&v)[4], const I8RowScale& r) {
     }
     constexpr float kMagic = 12582912.0f;
     const f32x2 inv = pack2(r.inv, r.inv), magic = pack2(kMagic, kMagic), minus = pack2(-1.0f, -1.0f);
-    float t[8];
+    uint32_t t[8];
     float far = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const f32x2 m = fma2(v[e], inv, magic);
-        const float2 d = unpack2(fma2(v[e], inv, fma2(m, minus, magic))), q = unpack2(m);
-        far = absmax3(far, d.x, d.y);
-        t[2 * e] = q.x;
-        t[2 * e + 1] = q.y;
+        if (EXACT) {
+            const float2 d = unpack2(fma2(v[e], inv, fma2(m, minus, magic)));
+            far = absmax3(far, d.x, d.y);
+        }
+        const float2 q = unpack2(m);
+        t[2 * e] = __float_as_uint(q.x);
+        t[2 * e + 1] = __float_as_uint(q.y);
     }
-    if (far > 0.5f - 0x1p-16f) {
+    if (EXACT && far > 0.5f - 0x1p-15f) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float2 vv = unpack2(v[e >> 1]);
-            const float ve = e & 1 ? vv.y : vv.x;
-            if (SHORT) {
-                const float q = t[e] - kMagic;
-                const float d = fmaf(-q, r.a, 127.0f * ve);
-                const float over = 2.0f * fabsf(d) - r.a;
-                const bool odd = (__float_as_uint(t[e]) & 1u) != 0;
-                if (over > 0.0f || (over == 0.0f && odd)) t[e] += copysignf(1.0f, d);
-            } else {
-                t[e] = __uint_as_float(static_cast<uint32_t>(i8_code_exact(ve, r.inv, r.a)));
-            }
+            t[e] = static_cast<uint32_t>(i8_code_exact(e & 1 ? vv.y : vv.x, r.inv, r.a));
         }
     }
-    uint32_t w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(t[e]);
-    return make_uint2(__byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410),
-                      __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040), 0x5410));
+    return make_uint2(__byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
 }
 
 __device__ __forceinline__ float absmax8(float m, const f32x2 (&v)[4]) {
@@ -158,9 +154,10 @@ __device__ __forceinline__ float absmax8(float m, const f32x2 (&v)[4]) {
 // v times eight channel scales, one rounding to fp32 each (the input gradient
 // folds the scales into dY).
 __device__ __forceinline__ void i8_scale8(const float* chan, f32x2 (&v)[4]) {
-    const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(chan));
-    const ulonglong2 b = __ldg(reinterpret_cast<const ulonglong2*>(chan) + 1);
-    v[0] = mul2(v[0], a.x), v[1] = mul2(v[1], a.y), v[2] = mul2(v[2], b.x), v[3] = mul2(v[3], b.y);
+    f32x2 c[4];
+    asm("ld.global.nc.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(c[0]), "=l"(c[1]), "=l"(c[2]), "=l"(c[3]) : "l"(chan));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], c[e]);
 }
 
 // Eight consecutive values of a row as they are stored.
@@ -192,21 +189,24 @@ struct I8Raw {
     }
 };
 
-// Few rows: one CTA per row, which stays in registers as it was stored (NV > 0:
-// at most 8 NV blockDim.x values) between its maximum and its codes, or is read
-// twice (NV == 0).  len % 8 == 0.
+// One CTA per row, which stays in registers (NV > 0: at most 8 NV THREADS values;
+// as they were stored, or scaled) between its maximum and its codes, or is read
+// twice (NV == 0).  Many rows keep 64 to 112 bytes a thread in flight with up to
+// 1024 threads per SM (4096 x 14336 bf16: 28 us, 0.96 of the copy rate; with
+// channel scales 43 us, bound by reading them and by the exact check); few rows
+// take as many threads as the row has pieces.  len % 8 == 0.
 // BESIDE: the kernel before this one (the adapter's product of the same call)
 // started after everything before it was complete and touches nothing of this
 // one's, so the two run side by side; waiting for it comes last, so that the
 // kernel after this one finds both complete.
 template <int SRC, bool SCALED, bool BESIDE, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) i8_quantize_rows_kernel(const void* __restrict__ in, int64_t len,
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) i8_quantize_rows_kernel(const void* __restrict__ in, int64_t len,
                                                                    const float* __restrict__ chan,
                                                                    int8_t* __restrict__ codes, int64_t ldc,
                                                                    float* __restrict__ scale) {
     constexpr int ESIZE = SRC == kSrcF32 ? 4 : 2;
     constexpr int KEEP = NV > 0 ? NV : 1;
-    constexpr bool SHORT = SRC != kSrcF32 && !SCALED;
+    constexpr bool EXACT = SRC != kSrcBf16 || SCALED;
     __shared__ uint32_t s_max[THREADS / 32];
     if (!BESIDE) griddep_wait();    // everything before this kernel is complete ...
     griddep_launch_dependents();    // ... so the kernel after it may read what came before
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(THREADS) i8_quantize_rows_kernel(const void* _
     const void* src = static_cast<const uint8_t*>(in) + row * len * ESIZE;
     int8_t* dst = codes + row * ldc;
     I8Raw<SRC> raw[KEEP];
+    f32x2 held[SCALED ? KEEP : 1][4];            // scaled values stay as they are, others as they were stored
     auto value8 = [&](const I8Raw<SRC>& x, int64_t j, f32x2 (&v)[4]) {
         x.values(v);
         if (SCALED) i8_scale8(chan + j * 8, v);
@@ -234,6 +235,10 @@ __global__ void __launch_bounds__(THREADS) i8_quantize_rows_kernel(const void* _
                 f32x2 v[4];
                 value8(raw[i], j, v);
                 top = absmax8(top, v);
+                if (SCALED) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) held[i][e] = v[e];
+                }
             }
         }
     } else {
@@ -256,9 +261,13 @@ __global__ void __launch_bounds__(THREADS) i8_quantize_rows_kernel(const void* _
         for (int i = 0; i < KEEP; ++i) {
             const int64_t j = threadIdx.x + static_cast<int64_t>(i) * THREADS;
             if (j < nvec) {
-                f32x2 v[4];
-                value8(raw[i], j, v);
-                *reinterpret_cast<uint2*>(dst + j * 8) = i8_codes8<SHORT>(v, r);
+                if (SCALED) {
+                    *reinterpret_cast<uint2*>(dst + j * 8) = i8_codes8<EXACT>(held[SCALED ? i : 0], r);
+                } else {
+                    f32x2 v[4];
+                    value8(raw[i], j, v);
+                    *reinterpret_cast<uint2*>(dst + j * 8) = i8_codes8<EXACT>(v, r);
+                }
             }
         }
     } else {
@@ -266,7 +275,7 @@ __global__ void __launch_bounds__(THREADS) i8_quantize_rows_kernel(const void* _
             f32x2 v[4];
             raw[0].load(src, j * 8);
             value8(raw[0], j, v);
-            *reinterpret_cast<uint2*>(dst + j * 8) = i8_codes8<SHORT>(v, r);
+            *reinterpret_cast<uint2*>(dst + j * 8) = i8_codes8<EXACT>(v, r);
         }
     }
     if (BESIDE) griddep_wait();

@@ -1134,9 +1134,9 @@ lbq_status lbq_quantize_i8(const void* X, int dtype, int rows, int k, int8_t* co
     if (!aligned16(X) || !aligned16(codes) || !aligned16(scale)) return LBQ_EALIGN;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     switch (dtype) {
-        case LBQ_F32: return run_i8_quantize<kSrcF32, false, false>(X, rows, k, nullptr, codes, k, scale, cs);
-        case LBQ_BF16: return run_i8_quantize<kSrcBf16, false, false>(X, rows, k, nullptr, codes, k, scale, cs);
-        case LBQ_F16: return run_i8_quantize<kSrcF16, false, false>(X, rows, k, nullptr, codes, k, scale, cs);
+        case LBQ_F32: return run_i8_quantize<kSrcF32, false, false>(X, rows, k, nullptr, codes, k, scale, sm_count(), cs);
+        case LBQ_BF16: return run_i8_quantize<kSrcBf16, false, false>(X, rows, k, nullptr, codes, k, scale, sm_count(), cs);
+        case LBQ_F16: return run_i8_quantize<kSrcF16, false, false>(X, rows, k, nullptr, codes, k, scale, sm_count(), cs);
     }
     return LBQ_EUNSUPPORTED;
 }
