@@ -4,11 +4,12 @@
 
 // Launch with optional cluster size and programmatic stream serialisation
 // (the kernel waits with griddepcontrol.wait before it reads what the kernel
-// before it wrote).  The kernel's shared memory limit is raised to the device's
-// once per device; setting it again, from another thread too, changes nothing.
+// before it wrote).  The kernel's limits (shared memory, clusters of more than 8)
+// are raised once per device; doing it again, from another thread too, changes
+// nothing.
 template <auto Kern, typename... Args>
 lbq_status launch_overlapped(dim3 grid, int threads, size_t smem, dim3 cluster, cudaStream_t st, const Args&... args) {
-    if (smem > 48 * 1024) {
+    if (smem > 48 * 1024 || cluster.x * cluster.y * cluster.z > 8) {
         static std::atomic<uint64_t> raised{0};
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return LBQ_ECUDA;
@@ -18,7 +19,8 @@ lbq_status launch_overlapped(dim3 grid, int threads, size_t smem, dim3 cluster, 
             cudaFuncAttributes fa;
             if (cudaFuncGetAttributes(&fa, Kern) != cudaSuccess ||
                 cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     227 * 1024 - static_cast<int>(fa.sharedSizeBytes)) != cudaSuccess) {
+                                     227 * 1024 - static_cast<int>(fa.sharedSizeBytes)) != cudaSuccess ||
+                cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
                 (void)cudaGetLastError();
                 return LBQ_ECUDA;
             }
@@ -95,7 +97,7 @@ lbq_status launch_i8_adapter(const void* in, int64_t m, int64_t len, const void*
                              cudaStream_t st) {
     // parts enough for two CTAs per SM
     const int64_t groups = cdiv(m, MT), chunks = cdiv(len, kAdChunk);
-    const int64_t parts = std::min<int64_t>({kAdMaxParts, chunks, std::max<int64_t>(1, 2 * sms / groups)});
+    const int64_t parts = std::min<int64_t>({MT <= 16 ? kAdMaxParts : 8, chunks, std::max<int64_t>(1, 2 * sms / groups)});
     return launch_overlapped<i8_adapter_kernel<COL, MT, R8>>(
         dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts)), kAdThreads, AdapterSmem<MT, R8>::kBytes,
         dim3(1, static_cast<unsigned>(parts), 1), st, static_cast<const uint16_t*>(in), m, static_cast<int>(len),
@@ -116,7 +118,7 @@ lbq_status launch_i8_adapter_tc(const void* in, int64_t m, int64_t len, const vo
                                       CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) return LBQ_ECUDA;
     const int64_t groups = cdiv(m, 128), blocks = cdiv(len, 64);
-    const int64_t parts = std::min<int64_t>({kAdMaxParts, blocks, std::max<int64_t>(1, sms / groups)});
+    const int64_t parts = std::min<int64_t>({8, blocks, std::max<int64_t>(1, sms / groups)});
     return launch_overlapped<i8_adapter_tc_kernel<COL, NR>>(
         dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts)), kAdTcThreads, AdapterTcSmem<NR>::kBytes,
         dim3(1, static_cast<unsigned>(parts), 1), st, tmX, tmW, static_cast<int>(m), static_cast<int>(len), r, out);

@@ -21,7 +21,7 @@ namespace lbq {
 
 constexpr int kAdThreads = 256;
 constexpr int kAdChunk = 128;
-constexpr int kAdMaxParts = 8;
+constexpr int kAdMaxParts = 16;          // few tokens: clusters beyond the portable size of 8
 
 template <int MT, int R8>
 struct AdapterSmem {
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kAdThreads) i8_adapter_kernel(const uint16_t* 
         if (t >= r || row0 + row >= m) continue;
         float v = 0.0f;
 #pragma unroll
-        for (int p = 0; p < kAdMaxParts; ++p) {
+        for (int p = 0; p < (MT <= 16 ? kAdMaxParts : 8); ++p) {
             if (p < parts) {
                 uint32_t remote;
                 float x;
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kAdTcThreads) i8_adapter_tc_kernel(const __gri
         const uint32_t at = smem_u32(smem) + (row * L::kRow + t) * 4;
         float v = 0.0f;
 #pragma unroll
-        for (int p = 0; p < kAdMaxParts; ++p) {
+        for (int p = 0; p < 8; ++p) {
             if (p < parts) {
                 uint32_t remote;
                 float x;

@@ -18,6 +18,8 @@
 // be the least exact part of the output).
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "dqgemm.cuh"
 #include "dqgemm_bwd.cuh"
@@ -266,27 +268,44 @@ __global__ void __launch_bounds__(kI8SplitThreads)
             tc_fence_before();
             __syncwarp();
             asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            // the cluster's sums of U tokens at a time, the next ones on their way meanwhile:
+            // about 32 loads in flight whatever the number of parts
             const uint32_t base = smem_u32(smem) + f * 4;
-#pragma unroll 1
-            for (int c = lo; c < hi; c += 4) {
-                int acc[4] = {0, 0, 0, 0};
+            auto join = [&](auto u_, auto parts_) {
+                constexpr int U = decltype(u_)::value, PARTS = decltype(parts_)::value;
+                int x[PARTS][U];
+                auto fetch = [&](int c) {
 #pragma unroll
-                for (int r = 0; r < kI8MaxSplit; ++r) {
-                    if (r < nsplit) {
-                        uint32_t remote;
-                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(base + c * 512), "r"(r));
+                    for (int r = 0; r < PARTS; ++r) {
+                        if (r < nsplit) {
+                            uint32_t remote;
+                            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(base + c * 512), "r"(r));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (c + i < hi) {
-                                int x;
-                                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(remote + i * 512) : "memory");
-                                acc[i] += x;
-                            }
+                            for (int i = 0; i < U; ++i)
+                                if (c + i < hi)
+                                    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x[r][i]) : "r"(remote + i * 512) : "memory");
                         }
                     }
+                };
+                if (lo < hi) fetch(lo);
+#pragma unroll 1
+                for (int c = lo; c < hi; c += U) {
+                    int acc[U];
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        acc[i] = 0;
+#pragma unroll
+                        for (int r = 0; r < PARTS; ++r)
+                            if (r < nsplit && c + i < hi) acc[i] += x[r][i];
+                    }
+                    if (c + U < hi) fetch(c + U);
+                    store(c, acc, hi - c);
                 }
-                store(c, acc, hi - c);
-            }
+            };
+            using std::integral_constant;
+            if (nsplit <= 2) join(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+            else if (nsplit <= 4) join(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+            else join(integral_constant<int, 4>{}, integral_constant<int, 8>{});
         }
     }
     tc_fence_before();
