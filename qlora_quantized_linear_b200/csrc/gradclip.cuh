@@ -198,6 +198,47 @@ __device__ __forceinline__ void grad_store_part(const ClipEntry& e, int64_t at, 
     }
 }
 
+// A chunk of whole pieces to an output that starts d bytes past a 16-byte
+// boundary: every lane joins the last d bytes of the piece before its own (its
+// neighbour's, or the last lane's previous one) with the first 16 - d of its
+// own and stores 16 aligned bytes.  The chunk's first 16 - d and last d bytes
+// go out in halfwords.  `o` is the lane's first piece.
+__device__ __forceinline__ void grad_store_shifted(uint8_t* o, const uint4 (&v)[kClipVecs], int d, int lane, uint64_t pol) {
+    const int s = 16 - d, wo = s >> 2, bits = (s & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < kClipVecs; ++i) {
+        const uint4 give = (lane == 31 && i > 0) ? v[i > 0 ? i - 1 : 0] : v[i];
+        uint32_t w[9];
+        w[0] = __shfl_sync(0xFFFFFFFFu, give.x, (lane + 31) & 31);
+        w[1] = __shfl_sync(0xFFFFFFFFu, give.y, (lane + 31) & 31);
+        w[2] = __shfl_sync(0xFFFFFFFFu, give.z, (lane + 31) & 31);
+        w[3] = __shfl_sync(0xFFFFFFFFu, give.w, (lane + 31) & 31);
+        w[4] = v[i].x, w[5] = v[i].y, w[6] = v[i].z, w[7] = v[i].w, w[8] = 0u;
+        if (wo & 1) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = w[j + 1];
+        }
+        if (wo & 2) {
+#pragma unroll
+            for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+        }
+        uint4 r;
+        r.x = __funnelshift_r(w[0], w[1], bits);
+        r.y = __funnelshift_r(w[1], w[2], bits);
+        r.z = __funnelshift_r(w[2], w[3], bits);
+        r.w = __funnelshift_r(w[3], w[4], bits);
+        if (i > 0 || lane > 0) st_hint(o + i * 512 - d, r, pol);
+    }
+    if (lane == 0 || lane == 31) {
+        const uint4 e = lane == 0 ? v[0] : v[kClipVecs - 1];
+        const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+        uint16_t* h = reinterpret_cast<uint16_t*>(lane == 0 ? o : o + (kClipVecs - 1) * 512);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (lane == 0 ? 2 * j < s : 2 * j >= s) h[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+    }
+}
+
 // A tensor of the range and what the walk over its chunks needs of it, in
 // registers: neighbouring chunks mostly belong to the same one.
 struct ClipCursor {
@@ -382,16 +423,22 @@ __global__ void __launch_bounds__(kClipThreads, 1)
         if (q >= kClipSlots) load(q - kClipSlots);
         if (coef == 1.0f && tc.g == tc.out) continue;           // in place and nothing to change
         uint8_t* o = tc.out + (at << (4 - tc.log_per));
-        const bool aligned = (reinterpret_cast<uintptr_t>(tc.out) & 15u) == 0;
+        const int d = static_cast<int>(reinterpret_cast<uintptr_t>(tc.out) & 15u);
 #pragma unroll
         for (int i = 0; i < kClipVecs; ++i) {
-            uint4 v;
-            v.x = grad_scale_word(r[i].x, tc.type, coef);
-            v.y = grad_scale_word(r[i].y, tc.type, coef);
-            v.z = grad_scale_word(r[i].z, tc.type, coef);
-            v.w = grad_scale_word(r[i].w, tc.type, coef);
-            if (whole && aligned) st_hint(o + i * 512, v, drop);
-            else grad_store_part(ent[tc.ti], at + (i * 32 << tc.log_per), v);
+            r[i].x = grad_scale_word(r[i].x, tc.type, coef);
+            r[i].y = grad_scale_word(r[i].y, tc.type, coef);
+            r[i].z = grad_scale_word(r[i].z, tc.type, coef);
+            r[i].w = grad_scale_word(r[i].w, tc.type, coef);
+        }
+        if (!whole) {
+#pragma unroll
+            for (int i = 0; i < kClipVecs; ++i) grad_store_part(ent[tc.ti], at + (i * 32 << tc.log_per), r[i]);
+        } else if (d == 0) {
+#pragma unroll
+            for (int i = 0; i < kClipVecs; ++i) st_hint(o + i * 512, r[i], drop);
+        } else {
+            grad_store_shifted(o, r, d, lane, drop);
         }
     }
 }
