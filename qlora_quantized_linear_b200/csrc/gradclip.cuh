@@ -10,7 +10,7 @@
 // 2 KB chunks of all tensors.  The tensors come as kernel arguments; a CTA
 // copies the few that its range meets to shared memory first (walking the
 // arguments where they are costs a constant-cache miss per step: 9 us of a
-// small call).  A warp takes every 32nd chunk of its CTA's range and feeds
+// small call).  A warp takes every 16th chunk of its CTA's range and feeds
 // itself by bulk copies through a ring of its own, so that the loads never wait
 // for the sums (192 KB in flight per SM).  Between the two phases the CTAs meet at a grid barrier (a cooperative
 // launch); what the rings hold by then is scaled without another read, and the
@@ -28,13 +28,13 @@ namespace lbq {
 
 enum GradType : int { kGradF32 = LBQ_F32, kGradBf16 = LBQ_BF16, kGradF16 = LBQ_F16 };
 
-constexpr int kClipThreads = 1024;
+constexpr int kClipThreads = 512;
 constexpr int kClipWarps = kClipThreads / 32;
 constexpr int kClipVecs = 4;                          // 16-byte pieces per lane and chunk
 constexpr int kClipChunk = kClipVecs * 32 * 16;       // 2 KB
-constexpr int kClipSlots = 3;                         // chunks of a warp's ring
+constexpr int kClipSlots = 6;                         // chunks of a warp's ring
 constexpr int kClipRing = kClipWarps * kClipSlots * kClipChunk;
-constexpr uint32_t kClipL2 = 64u << 20;               // bytes of a launch that are held in L2 between the phases
+constexpr uint32_t kClipL2 = 80u << 20;               // bytes of a launch that are held in L2 between the phases
 constexpr int kClipMaxCtas = 256;                     // CTAs of a launch
 constexpr int kClipTable = 976;                       // tensors per launch (kernel arguments are below 32764 bytes)
 
@@ -73,68 +73,103 @@ struct ClipWork {
 
 enum ClipMode : int { kClipSum = 0, kClipSumLast = 1, kClipScale = 2, kClipFused = 3 };
 
-__device__ __forceinline__ float grad_f32(uint32_t w, int type, int hi) {
-    if (type == kGradF32) return __uint_as_float(w);
+template <int TYPE>
+__device__ __forceinline__ float grad_f32(uint32_t w, int hi) {
+    if (TYPE == kGradF32) return __uint_as_float(w);
     const uint32_t h = hi ? w >> 16 : w & 0xFFFFu;
-    return type == kGradBf16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(static_cast<uint16_t>(h));
+    return TYPE == kGradBf16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(static_cast<uint16_t>(h));
 }
 
 // Sum of the squares of a 16-byte piece in fp32: chains of four.
-__device__ __forceinline__ float grad_sumsq32(const uint4& r, int type) {
+template <int TYPE>
+__device__ __forceinline__ float grad_sumsq32(const uint4& r) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     float s = 0.0f, t = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = grad_f32(w[i], type, 0);
+        const float a = grad_f32<TYPE>(w[i], 0);
         s = fmaf(a, a, s);
     }
-    if (type != kGradF32) {
+    if (TYPE != kGradF32) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float b = grad_f32(w[i], type, 1);
+            const float b = grad_f32<TYPE>(w[i], 1);
             t = fmaf(b, b, t);
         }
     }
     return s + t;
 }
 
-__device__ __forceinline__ double grad_sumsq64(const uint4& r, int type) {
+template <int TYPE>
+__device__ __forceinline__ double grad_sumsq64(const uint4& r) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
     double d = 0.0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const double a = grad_f32(w[i], type, 0);
+        const double a = grad_f32<TYPE>(w[i], 0);
         d = fma(a, a, d);
-        if (type != kGradF32) {
-            const double b = grad_f32(w[i], type, 1);
+        if (TYPE != kGradF32) {
+            const double b = grad_f32<TYPE>(w[i], 1);
             d = fma(b, b, d);
         }
     }
     return d;
 }
 
+// The same of four pieces in fp64; out of line, so that no part of it runs
+// where it is not needed.
+template <int TYPE>
+__device__ __noinline__ double grad_sumsq_far(uint4 a, uint4 b, uint4 c, uint4 d) {
+    return (grad_sumsq64<TYPE>(a) + grad_sumsq64<TYPE>(b)) + (grad_sumsq64<TYPE>(c) + grad_sumsq64<TYPE>(d));
+}
+
 // Of a lane's four pieces.  In fp32 it is safe when it lies in [2^-66, 2^100]:
 // no square overflowed and what squares below the normal range lost is under
 // 2^-50 of it.
-__device__ __forceinline__ double grad_sumsq(const uint4 (&r)[4], int type) {
-    const float s = (grad_sumsq32(r[0], type) + grad_sumsq32(r[1], type)) +
-                    (grad_sumsq32(r[2], type) + grad_sumsq32(r[3], type));
-    if (s >= 0x1p-66f && s <= 0x1p100f) return static_cast<double>(s);
-    uint32_t any = 0u;
+template <int TYPE>
+__device__ __forceinline__ double grad_sumsq(const uint4 (&r)[4]) {
+    const float s = (grad_sumsq32<TYPE>(r[0]) + grad_sumsq32<TYPE>(r[1])) +
+                    (grad_sumsq32<TYPE>(r[2]) + grad_sumsq32<TYPE>(r[3]));
+    double d = static_cast<double>(s);
+    if (!(s >= 0x1p-66f && s <= 0x1p100f)) {
+        uint32_t any = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) any |= r[i].x | r[i].y | r[i].z | r[i].w;
-    if (any == 0u) return 0.0;
-    double d = 0.0;
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) d += grad_sumsq64(i == 0 ? r[0] : i == 1 ? r[1] : i == 2 ? r[2] : r[3], type);
+        for (int i = 0; i < 4; ++i) any |= r[i].x | r[i].y | r[i].z | r[i].w;
+        d = 0.0;
+        if (any != 0u) d = grad_sumsq_far<TYPE>(r[0], r[1], r[2], r[3]);
+    }
     return d;
 }
 
-__device__ __forceinline__ uint32_t grad_scale_word(uint32_t w, int type, float c) {
-    if (type == kGradF32) return __float_as_uint(__fmul_rn(__uint_as_float(w), c));
-    const float a = __fmul_rn(grad_f32(w, type, 0), c), b = __fmul_rn(grad_f32(w, type, 1), c);
-    if (type == kGradBf16) return pack_bf16x2_rn(a, b);
+template <int TYPE>
+__device__ __forceinline__ uint32_t grad_scale_word(uint32_t w, float c) {
+    if (TYPE == kGradF32) return __float_as_uint(__fmul_rn(__uint_as_float(w), c));
+    const float a = __fmul_rn(grad_f32<TYPE>(w, 0), c), b = __fmul_rn(grad_f32<TYPE>(w, 1), c);
+    if (TYPE == kGradBf16) return pack_bf16x2_rn(a, b);
     return static_cast<uint32_t>(f32_to_f16_bits(a)) | (static_cast<uint32_t>(f32_to_f16_bits(b)) << 16);
+}
+
+// By the tensor's type, once per chunk.
+__device__ __forceinline__ double grad_sumsq_of(const uint4 (&r)[4], int type) {
+    if (type == kGradF32) return grad_sumsq<kGradF32>(r);
+    return type == kGradBf16 ? grad_sumsq<kGradBf16>(r) : grad_sumsq<kGradF16>(r);
+}
+
+template <int TYPE>
+__device__ __forceinline__ void grad_scale(uint4 (&r)[4], float c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[i].x = grad_scale_word<TYPE>(r[i].x, c);
+        r[i].y = grad_scale_word<TYPE>(r[i].y, c);
+        r[i].z = grad_scale_word<TYPE>(r[i].z, c);
+        r[i].w = grad_scale_word<TYPE>(r[i].w, c);
+    }
+}
+
+__device__ __forceinline__ void grad_scale_of(uint4 (&r)[4], int type, float c) {
+    if (type == kGradF32) grad_scale<kGradF32>(r, c);
+    else if (type == kGradBf16) grad_scale<kGradBf16>(r, c);
+    else grad_scale<kGradF16>(r, c);
 }
 
 // L2 eviction policies: pieces that are read again in the same launch stay as
@@ -370,7 +405,7 @@ __global__ void __launch_bounds__(kClipThreads, 1)
             pieces(q, at, r);
             __syncwarp();                                       // the slot is read
             if (q + kClipSlots < nq) load(q + kClipSlots);
-            acc += grad_sumsq(r, tc.type);
+            acc += grad_sumsq_of(r, tc.type);
         }
         const double mine = cta_sum(acc, s_sum);
         if (threadIdx.x == 0) {
@@ -424,13 +459,7 @@ __global__ void __launch_bounds__(kClipThreads, 1)
         if (coef == 1.0f && tc.g == tc.out) continue;           // in place and nothing to change
         uint8_t* o = tc.out + (at << (4 - tc.log_per));
         const int d = static_cast<int>(reinterpret_cast<uintptr_t>(tc.out) & 15u);
-#pragma unroll
-        for (int i = 0; i < kClipVecs; ++i) {
-            r[i].x = grad_scale_word(r[i].x, tc.type, coef);
-            r[i].y = grad_scale_word(r[i].y, tc.type, coef);
-            r[i].z = grad_scale_word(r[i].z, tc.type, coef);
-            r[i].w = grad_scale_word(r[i].w, tc.type, coef);
-        }
+        grad_scale_of(r, tc.type, coef);
         if (!whole) {
 #pragma unroll
             for (int i = 0; i < kClipVecs; ++i) grad_store_part(ent[tc.ti], at + (i * 32 << tc.log_per), r[i]);

@@ -86,7 +86,12 @@ constexpr int kI8MaxSplit = 8;
 constexpr int kI8SplitMaxStages = 12;
 
 // Shared memory of a CTA: the ring (the partial sums reuse it), the token
-// scales, s T of the CTA's share of the tokens, the barriers.
+// scales, s T of the CTA's share of the tokens, the barriers.  Tiles of more
+// than 128 tokens take over half of the SM's, whatever their ring: CTAs of 256
+// tensor memory columns that wait for one another in clusters must not meet
+// three to an SM, where one could wait for columns that only its partner's
+// partner frees.  (With at most 128 columns each, shared memory admits no more
+// CTAs than the 512 columns hold, beside this library's other kernels too.)
 struct I8SplitShape {
     int nt, stages, tok;
     __host__ __device__ int stage_bytes() const { return 128 * 128 + nt * 128; }
@@ -95,7 +100,8 @@ struct I8SplitShape {
         return stages * stage_bytes() > sums ? stages * stage_bytes() : sums;
     }
     __host__ __device__ size_t bytes(int rp) const {
-        return static_cast<size_t>(ring()) + nt * 4 + static_cast<size_t>(tok) * rp * 4 + (2 * stages + 1) * 8 + 16 + 1024;
+        const size_t b = static_cast<size_t>(ring()) + nt * 4 + static_cast<size_t>(tok) * rp * 4 + (2 * stages + 1) * 8 + 16 + 1024;
+        return nt > 128 && b < 116 * 1024 ? 116 * 1024 : b;
     }
 };
 
@@ -662,7 +668,8 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
     } else {
         // ------------------------------------------------------------ epilogue
         // lane = output feature: 128 contiguous bytes of Y per token; a warp takes
-        // 32 features and half of the tokens
+        // 32 features and half of the tokens.  Y is stored to leave L2 first: the
+        // weight is read again for every 256 tokens
         griddep_wait();
         const int quarter = warp & 3, half = (warp - 2) >> 2, tid = threadIdx.x - 64;
         float* sx = reinterpret_cast<float*>(smem + C::kScale) + (warp - 2) * 128;   // the warp's copy (no adapter)
@@ -707,7 +714,7 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
                     if (c == 96) arrive(&dempty[buf]);        // the last columns are in registers
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        if (ok && c + i < live) *row = static_cast<float>(static_cast<int>(r[i])) * sx[c + i] * so;
+                        if (ok && c + i < live) __stcs(row, static_cast<float>(static_cast<int>(r[i])) * sx[c + i] * so);
                         row += p.out;
                     }
                     __syncwarp();
@@ -735,7 +742,7 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
                     if (q == 3) arrive(&dempty[buf]);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        if (ok && 32 * q + i < live) *row = __uint_as_float(r[q][i]) + __uint_as_float(d[i]);
+                        if (ok && 32 * q + i < live) __stcs(row, __uint_as_float(r[q][i]) + __uint_as_float(d[i]));
                         row += p.out;
                     }
                     __syncwarp();
