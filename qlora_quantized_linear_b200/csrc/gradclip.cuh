@@ -12,9 +12,16 @@
 // arguments where they are costs a constant-cache miss per step: 9 us of a
 // small call).  A warp takes every 16th chunk of its CTA's range and feeds
 // itself by bulk copies through a ring of its own, so that the loads never wait
-// for the sums (192 KB in flight per SM).  Between the two phases the CTAs meet at a grid barrier (a cooperative
-// launch); what the rings hold by then is scaled without another read, and the
-// rest is read again from the last chunk backwards, the latest of it from L2.
+// for the sums (192 KB in flight per SM).  Between the two phases the CTAs meet
+// at a grid barrier (a cooperative launch); what the rings hold by then is
+// scaled without another read, and the rest is read again from the last chunk
+// backwards, the latest of it from L2.
+//
+// Measured: 42 M fp32 values in 448 tensors in 85 us.  Each value read and
+// written once is 51 us at the copy rate; the second read of what neither the
+// rings nor L2 held (105 MB of 168) makes it 67 us, and the ramps of the two
+// phases and the barrier between them the rest.  168 M bf16 values in 448
+// tensors: 172 us, 103 us at one read and one write.
 //
 // The squares of a lane's four 16-byte pieces of a chunk are added in fp32, in
 // chains of four and then in pairs (at most 7 roundings), when the sum is in a
