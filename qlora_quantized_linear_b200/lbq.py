@@ -12,6 +12,7 @@ and every call raises `LbqError` when the library returns a non-OK status.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -193,6 +194,13 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
+
+
+def _on(stream):
+    """Makes a caller's stream the current one while a helper allocates and launches: a temporary is then filled in
+    that stream's order and its memory goes back to that stream."""
+    torch = _torch()
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _bf16_2d(t, name):
@@ -528,11 +536,12 @@ def quantize_i8(X, codes=None, scale=None, stream=None):
         raise ValueError("X must be a contiguous 2-D CUDA tensor")
     code = _dtype_code(X, "X")
     rows, k = X.shape
-    codes = _out(codes, (rows, k), torch.int8, "codes", X)
-    scale = _out(scale, (rows,), torch.float32, "scale", X)
-    _same_device(X.device, codes=codes, scale=scale)
-    _check(lbq_quantize_i8(X.data_ptr(), code, rows, k, codes.data_ptr(), scale.data_ptr(), _stream(stream)),
-           "lbq_quantize_i8")
+    with _on(stream):
+        codes = _out(codes, (rows, k), torch.int8, "codes", X)
+        scale = _out(scale, (rows,), torch.float32, "scale", X)
+        _same_device(X.device, codes=codes, scale=scale)
+        _check(lbq_quantize_i8(X.data_ptr(), code, rows, k, codes.data_ptr(), scale.data_ptr(), _stream(None)),
+               "lbq_quantize_i8")
     return codes, scale
 
 
@@ -591,6 +600,10 @@ def _f32_out(t, m, n, name, like):
 
 def _linear_i8(call, what, space, x, name, width_in, width_out, qw, A, B, s, out, out_name, saved, saved_name,
                workspace, stream):
+    if stream is not None:
+        with _on(stream):
+            return _linear_i8(call, what, space, x, name, width_in, width_out, qw, A, B, s, out, out_name, saved,
+                              saved_name, workspace, None)
     torch = _torch()
     dev, bf16 = qw.device_index, torch.bfloat16
     if x.dtype is not bf16 or x.dim() != 2 or not x.is_contiguous():
@@ -621,7 +634,7 @@ def _linear_i8(call, what, space, x, name, width_in, width_out, qw, A, B, s, out
     # the library launches on the current device
     if dev != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on cuda:{dev}, not on the current CUDA device")
-    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    st = torch._C._cuda_getCurrentRawStream(dev)
     rc = call(x.data_ptr(), m, qw._ref, a, b, rank, s, out.data_ptr(), t, workspace.data_ptr(), workspace.nbytes, st)
     if rc != LBQ_OK:
         raise LbqError(rc, what)
@@ -647,7 +660,8 @@ class GradClip:
     """The norm and the clipping of one list of gradients, step after step: keeps the list's table, the norm and
     the workspace.  `grads` are contiguous fp32, bf16 or fp16 CUDA tensors; `outs` (default: the gradients
     themselves) get the scaled copies, with the same types and sizes.  The tensors are held, so their memory
-    stays theirs; calls of one GradClip that may run at the same time race on its workspace."""
+    stays theirs; calls of one GradClip that may run at the same time race on its workspace, which is zeroed on
+    the stream that is current here: a call on another stream has to come after that."""
 
     def __init__(self, grads, outs=None):
         torch = _torch()
@@ -694,12 +708,14 @@ class GradClip:
 
 def grad_norm(grads, stream=None):
     """The Euclidean norm of all `grads` together (fp32 [1], on the device)."""
-    return GradClip(grads).norm(stream=stream)
+    with _on(stream):
+        return GradClip(grads).norm()
 
 
 def clip_grad_norm(grads, max_norm: float, outs=None, stream=None):
     """Clip `grads` to max_norm, in place or into `outs`; returns their norm before (fp32 [1], on the device)."""
-    return GradClip(grads, outs).clip(max_norm, stream=stream)
+    with _on(stream):
+        return GradClip(grads, outs).clip(max_norm)
 
 
 def device_status() -> int:

@@ -208,3 +208,27 @@ def test_helpers_refuse(lbq):
         with pytest.raises(lbq.LbqError):
             bad()
     assert abs(lbq.grad_norm([a, a]).item() - math.sqrt(2) * ref_norm([a])) <= 5 * STEP * 2 * ref_norm([a])
+
+
+def test_helpers_own_the_order_on_another_stream(lbq):
+    """clip_grad_norm and grad_norm on a stream that is not the current one, which is busy: their workspace is zeroed
+    and given back in the order of the call's stream."""
+    side = torch.cuda.Stream()
+    grads = [normal(n, 0.5, n) for n in (70001, 33, 4096)]
+    want = ref_norm(grads)
+    copies = [[g.clone() for g in grads] for _ in range(6)]
+    big = normal(1 << 26, 1.0, 1)
+    dirt = torch.full((1 << 20,), 0x5A, dtype=torch.uint8, device="cuda")
+    del dirt                                       # memory of the current stream that a workspace may take
+    torch.cuda.synchronize()
+    for _ in range(20):
+        big.mul_(1.0001)                           # the current stream is milliseconds behind
+    norms = [lbq.clip_grad_norm(c, 1.0, stream=side) for c in copies] + [lbq.grad_norm(grads, stream=side)]
+    torch.cuda.synchronize()
+    for n in norms:
+        assert norm_is(n.item(), want)
+    coef = 1.0 / (want + 1e-6)
+    for c in copies:
+        for g, o in zip(grads, c):
+            assert bool(((o.double() - g.double() * coef).abs() <= 7 * STEP * g.double().abs() * coef).all())
+    assert lbq.device_status() == 0

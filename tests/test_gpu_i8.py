@@ -334,6 +334,28 @@ def test_back_to_back_calls_and_streams(lbq):
     assert lbq.device_status() == 0
 
 
+def test_temporaries_on_another_stream(lbq):
+    """Calls on a stream that is not the current one, with outputs and workspaces of the helpers' own, while the
+    current stream takes and writes memory too."""
+    n, k, m, r = 512, 4096, 24, 8
+    codes, scale, A, B = layer(n, k, r, 31)
+    qw = lbq.Int8Weight(n, k, codes=codes, scale=scale)
+    X, dY, W = normal((m, k), 1.0, 32), normal((m, n), 0.1, 33), normal((64, k), 1.0, 34)
+    want = [t.clone() for t in lbq.linear_i8_fwd(X, qw, A, B, 1.0) + lbq.linear_i8_bwd(dY, qw, A, B, 1.0) + lbq.quantize_i8(W)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got, other = [], []
+    for _ in range(10):
+        got.append(lbq.linear_i8_fwd(X, qw, A, B, 1.0, stream=side) + lbq.linear_i8_bwd(dY, qw, A, B, 1.0, stream=side) +
+                   lbq.quantize_i8(W, stream=side))
+        other.append(torch.full((m * k + 4096,), 0x7F, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a, b)
+    assert lbq.device_status() == 0
+
+
 def test_helpers_refuse(lbq):
     n, k, m = 64, 32, 4
     qw = lbq.Int8Weight(n, k).quantize(normal((n, k), 1.0, 1))
