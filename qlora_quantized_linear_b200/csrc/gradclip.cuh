@@ -351,9 +351,9 @@ __global__ void __launch_bounds__(kClipThreads, 1)
     // the tensors of this range, from the arguments to shared memory by all threads at once
     ClipEntry* ent = reinterpret_cast<ClipEntry*>(clip_smem + kClipRing);
     const int f0 = tab.first[blockIdx.x], fn = tab.count > 0 ? tab.first[blockIdx.x + 1] - f0 + 1 : 0;
-    if (threadIdx.x < fn) {
-        const uint4* src = reinterpret_cast<const uint4*>(tab.e + f0 + threadIdx.x);
-        uint4* dst = reinterpret_cast<uint4*>(ent + threadIdx.x);
+    for (int i = threadIdx.x; i < fn; i += kClipThreads) {
+        const uint4* src = reinterpret_cast<const uint4*>(tab.e + f0 + i);
+        uint4* dst = reinterpret_cast<uint4*>(ent + i);
         dst[0] = ld_generic(src);
         dst[1] = ld_generic(src + 1);
     }

@@ -109,6 +109,23 @@ def test_many_tensors_of_all_types(lbq):
         assert abs(plan.norm().item() - ref_norm(grads)) <= 5 * STEP * ref_norm(grads)
 
 
+def test_many_small_tensors_in_one_range(lbq):
+    """900 tensors of one element before a large one: the first CTA's equal share of the bytes meets all of them, more
+    tensors than it has threads."""
+    small = [torch.full((1,), 0.25 + 0.125 * (i % 7), device="cuda") for i in range(900)]
+    large = torch.full((80_000_000,), 2.0 ** -10, device="cuda")
+    want = math.sqrt(sum(float(t) ** 2 for t in small) + 80_000_000 * 2.0 ** -20)
+    flat = torch.cat(small)
+    norm = lbq.clip_grad_norm(small + [large], 1.0)
+    torch.cuda.synchronize()
+    assert norm_is(norm.item(), want)
+    coef = 1.0 / (want + 1e-6)
+    got = torch.cat(small).double()
+    assert bool(((got - flat.double() * coef).abs() <= 7 * STEP * got).all())
+    assert bool(((large.double() - 2.0 ** -10 * coef).abs() <= 7 * STEP * 2.0 ** -10 * coef).all())
+    assert lbq.device_status() == 0
+
+
 @pytest.mark.parametrize("scale", [1e-42, 1e-30, 1e-20, 1e-5, 1e15, 1e25, 1e37])
 def test_magnitudes(lbq, scale):
     """Squares below and above the range of fp32."""
