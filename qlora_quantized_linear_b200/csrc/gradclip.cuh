@@ -351,13 +351,20 @@ __global__ void __launch_bounds__(kClipThreads, 1)
     // the tensors of this range, from the arguments to shared memory by all threads at once
     ClipEntry* ent = reinterpret_cast<ClipEntry*>(clip_smem + kClipRing);
     const int f0 = tab.first[blockIdx.x], fn = tab.count > 0 ? tab.first[blockIdx.x + 1] - f0 + 1 : 0;
-    for (int i = threadIdx.x; i < fn; i += kClipThreads) {
-        const uint4* src = reinterpret_cast<const uint4*>(tab.e + f0 + i);
-        uint4* dst = reinterpret_cast<uint4*>(ent + i);
-        dst[0] = ld_generic(src);
-        dst[1] = ld_generic(src + 1);
+    bool same = true;
+#pragma unroll
+    for (int i0 = 0; i0 < CAP; i0 += kClipThreads) {
+        const int i = i0 + static_cast<int>(threadIdx.x);
+        if (i < fn) {
+            const uint4* src = reinterpret_cast<const uint4*>(tab.e + f0 + i);
+            uint4* dst = reinterpret_cast<uint4*>(ent + i);
+            const uint4 p = ld_generic(src);                    // g, out
+            same &= p.x == p.z && p.y == p.w;
+            dst[0] = p;
+            dst[1] = ld_generic(src + 1);
+        }
     }
-    __syncthreads();
+    const bool inplace = __syncthreads_and(same);           // of the whole range
     const uint64_t drop = l2_policy(false), hold = l2_policy(true);
     const int held = cn - static_cast<int>(kClipL2 / kClipChunk / gridDim.x);      // first chunk to hold in L2
     // the whole pieces of chunk q to its slot; piece p of a tensor holds the
@@ -452,6 +459,7 @@ __global__ void __launch_bounds__(kClipThreads, 1)
     // min(1, x) that keeps a NaN
     const double ratio = static_cast<double>(wk.max_norm) / (norm + 1e-6);
     const float coef = ratio > 1.0 ? 1.0f : static_cast<float>(ratio);
+    if (coef == 1.0f && inplace) return;                    // nothing to change, and no load is in flight
     if (MODE == kClipScale)
         for (int q = nq - 1; q >= 0 && q >= nq - kClipSlots; --q) load(q);
     for (int q = nq - 1; q >= 0; --q) {
@@ -463,7 +471,7 @@ __global__ void __launch_bounds__(kClipThreads, 1)
         const bool whole = pieces(q, at, r);
         __syncwarp();                                           // the slot is read
         if (q >= kClipSlots) load(q - kClipSlots);
-        if (coef == 1.0f && tc.g == tc.out) continue;           // in place and nothing to change
+        if (coef == 1.0f && tc.g == tc.out) continue;           // this tensor is in place
         uint8_t* o = tc.out + (at << (4 - tc.log_per));
         const int d = static_cast<int>(reinterpret_cast<uintptr_t>(tc.out) & 15u);
         grad_scale_of(r, tc.type, coef);

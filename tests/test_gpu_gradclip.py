@@ -249,3 +249,15 @@ def test_helpers_own_the_order_on_another_stream(lbq):
         for g, o in zip(grads, c):
             assert bool(((o.double() - g.double() * coef).abs() <= 7 * STEP * g.double().abs() * coef).all())
     assert lbq.device_status() == 0
+
+
+def test_some_in_place_some_not_and_nothing_to_clip(lbq):
+    """Below max_norm the tensors in place keep their bits and the others are copied, also within one CTA's range."""
+    grads = [normal(n, 0.01, n) for n in (3, 700_001, 40, 5000, 9)]
+    outs = [g if i % 2 else torch.full_like(g, 7.0) for i, g in enumerate(grads)]
+    before = [g.clone() for g in grads]
+    lbq.clip_grad_norm(grads, 1e9, outs)
+    torch.cuda.synchronize()
+    for g, o, b in zip(grads, outs, before):
+        assert torch.equal(g, b) and torch.equal(o, b)
+    assert lbq.device_status() == 0
