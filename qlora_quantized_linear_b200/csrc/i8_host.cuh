@@ -2,30 +2,34 @@
 // choice of kernel and split, tensor maps and launches.  Included by lbq.cu
 // inside its anonymous namespace.
 
+// Raises a kernel's limits (shared memory to what its own leaves of the 227 KB,
+// clusters of more than 8) once per device; doing it again, from another thread
+// too, changes nothing.
+template <auto Kern>
+bool raise_limits(int dev) {
+    static std::atomic<uint64_t> raised{0};
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev <= 63 && (raised.load(std::memory_order_relaxed) & bit)) return true;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, Kern) != cudaSuccess ||
+        cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             227 * 1024 - static_cast<int>(fa.sharedSizeBytes)) != cudaSuccess ||
+        cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return false;
+    }
+    raised.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
 // Launch with optional cluster size and programmatic stream serialisation
 // (the kernel waits with griddepcontrol.wait before it reads what the kernel
-// before it wrote).  The kernel's limits (shared memory, clusters of more than 8)
-// are raised once per device; doing it again, from another thread too, changes
-// nothing.
+// before it wrote).
 template <auto Kern, typename... Args>
 lbq_status launch_overlapped(dim3 grid, int threads, size_t smem, dim3 cluster, cudaStream_t st, const Args&... args) {
     if (smem > 48 * 1024 || cluster.x * cluster.y * cluster.z > 8) {
-        static std::atomic<uint64_t> raised{0};
         int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return LBQ_ECUDA;
-        const uint64_t bit = uint64_t(1) << (dev & 63);
-        if (dev > 63 || !(raised.load(std::memory_order_relaxed) & bit)) {
-            // what the kernel's own shared memory leaves of the 227 KB
-            cudaFuncAttributes fa;
-            if (cudaFuncGetAttributes(&fa, Kern) != cudaSuccess ||
-                cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     227 * 1024 - static_cast<int>(fa.sharedSizeBytes)) != cudaSuccess ||
-                cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-                (void)cudaGetLastError();
-                return LBQ_ECUDA;
-            }
-            raised.fetch_or(bit, std::memory_order_relaxed);
-        }
+        if (cudaGetDevice(&dev) != cudaSuccess || !raise_limits<Kern>(dev)) return LBQ_ECUDA;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -49,6 +53,46 @@ lbq_status launch_overlapped(dim3 grid, int threads, size_t smem, dim3 cluster, 
         return LBQ_ECUDA;
     }
     return LBQ_OK;
+}
+
+// How many clusters of `parts` CTAs (at most 8) run at the same time, per_sm (1
+// or 2) CTAs to an SM: a cluster stays within a group of SMs, and the groups
+// are of several sizes, so clusters leave SMs over.  (Sixteen clusters of 8 do not
+// fit one CTA per SM: the adapter product of 2048 tokens x 28672 at rank 16 took
+// two waves, 55 us, and takes one of 16 clusters of 6, 36 us.)  Asked once per
+// device, for a kernel of no tensor memory with that much shared memory: the
+// answer for one that has it counted a single CTA per SM.
+int clusters_that_fit(int parts, int per_sm, int sms) {
+    static std::atomic<int> known[16][2][kI8MaxSplit + 1];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return per_sm * sms / parts;
+    std::atomic<int>* slot = dev < 16 ? &known[dev][per_sm - 1][parts] : nullptr;
+    if (slot && (n = slot->load(std::memory_order_relaxed)) > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, 1, static_cast<unsigned>(parts));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = (per_sm == 1 ? 116 : 106) * 1024;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = static_cast<unsigned>(parts);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    constexpr auto kern = i8_quantize_rows_kernel<kSrcBf16, false, false, 1, 256>;
+    if (!raise_limits<kern>(dev) || cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = per_sm * sms / parts;
+    }
+    if (slot) slot->store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// The largest number of parts up to `most` whose clusters, `count` of them, run
+// at the same time.
+int parts_that_fit(int64_t most, int64_t count, int per_sm, int sms) {
+    int parts = static_cast<int>(most);
+    while (parts > 1 && clusters_that_fit(parts, per_sm, sms) < count) --parts;
+    return parts;
 }
 
 lbq_status check_i8weight(const lbq_i8weight* q, bool need_data) {
@@ -95,9 +139,12 @@ lbq_status run_i8_quantize(const void* in, int64_t rows, int64_t len, const floa
 template <bool COL, int MT, int R8>
 lbq_status launch_i8_adapter(const void* in, int64_t m, int64_t len, const void* wt, int r, float* out, int sms,
                              cudaStream_t st) {
-    // parts enough for two CTAs per SM
+    // one token tile: as many parts as a cluster holds; more: parts that fill the SMs
     const int64_t groups = cdiv(m, MT), chunks = cdiv(len, kAdChunk);
-    const int64_t parts = std::min<int64_t>({MT <= 16 ? kAdMaxParts : 8, chunks, std::max<int64_t>(1, 2 * sms / groups)});
+    constexpr int kPerSm = AdapterSmem<MT, R8>::kBytes <= 106 * 1024 ? 2 : 1;
+    const int64_t parts =
+        MT <= 16 ? std::min<int64_t>(kAdMaxParts, chunks)
+                 : parts_that_fit(std::min<int64_t>({8, chunks, std::max<int64_t>(1, kPerSm * sms / groups)}), groups, kPerSm, sms);
     return launch_overlapped<i8_adapter_kernel<COL, MT, R8>>(
         dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts)), kAdThreads, AdapterSmem<MT, R8>::kBytes,
         dim3(1, static_cast<unsigned>(parts), 1), st, static_cast<const uint16_t*>(in), m, static_cast<int>(len),
@@ -118,7 +165,7 @@ lbq_status launch_i8_adapter_tc(const void* in, int64_t m, int64_t len, const vo
                                       CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) return LBQ_ECUDA;
     const int64_t groups = cdiv(m, 128), blocks = cdiv(len, 64);
-    const int64_t parts = std::min<int64_t>({8, blocks, std::max<int64_t>(1, sms / groups)});
+    const int64_t parts = parts_that_fit(std::min<int64_t>({8, blocks, std::max<int64_t>(1, sms / groups)}), groups, 1, sms);
     return launch_overlapped<i8_adapter_tc_kernel<COL, NR>>(
         dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts)), kAdTcThreads, AdapterTcSmem<NR>::kBytes,
         dim3(1, static_cast<unsigned>(parts), 1), st, tmX, tmW, static_cast<int>(m), static_cast<int>(len), r, out);
@@ -191,8 +238,8 @@ I8Plan plan_i8(int m, int64_t out, int64_t red, int sms) {
     pl.sh.nt = static_cast<int>(round_up(static_cast<size_t>(cdiv(m, ttiles)), 16));
     // two CTAs per SM while their rings hold three blocks each
     const int per_sm = pl.sh.nt <= 128 ? 2 : 1;
-    const int64_t want = std::max<int64_t>(1, per_sm * sms / (rtiles * cdiv(m, pl.sh.nt)));
-    pl.nsplit = static_cast<int>(std::min<int64_t>(want, smax));
+    const int64_t tiles = rtiles * cdiv(m, pl.sh.nt), want = std::max<int64_t>(1, per_sm * sms / tiles);
+    pl.nsplit = parts_that_fit(std::min<int64_t>(want, smax), tiles, per_sm, sms);
     pl.sh.tok = static_cast<int>(cdiv(pl.sh.nt, pl.nsplit));
     return pl;
 }

@@ -178,10 +178,12 @@ SIZES = [
     (513, 2000, 640, 16),
     # enough tiles for the paired kernel, ragged in both directions
     (2600, 2000, 160, 0), (2600, 2000, 160, 7), (2305, 2561, 1168, 16), (2305, 2568, 400, 64),
-    # several waves of tiles, the last ones shared between pairs
+    # several waves of tiles
     (4200, 4208, 272, 0), (4110, 4368, 528, 16),
     # clusters of 3, 5, 6 and 7 parts in the forward
     (5, 12000, 2048, 8), (5, 6400, 4096, 0), (20, 6000, 4096, 4), (7, 5200, 4096, 16),
+    # parts that the GPU's groups of SMs hold at the same time
+    (8, 5100, 4096, 0), (300, 2304, 4096, 0), (2048, 2048, 2048, 16), (2155, 2000, 192, 33),
     # many tokens and few features: small token tiles, one part of the reduction
     (3913, 78, 64, 64), (1500, 40, 32, 0), (904, 1500, 224, 33), (1015, 300, 2000, 16), (260, 16, 1456, 64),
 ]
