@@ -229,12 +229,15 @@ I8Plan plan_i8(int m, int64_t out, int64_t red, int sms) {
         pl.pair = true;
         return pl;
     }
-    // token tiles of at most 256, smaller ones (down to 32) where the output features and
-    // the parts of the reduction leave SMs idle: 3913 tokens x 78 x 64, rank 64, took 82 us
-    // on 16 CTAs of 256 tokens
+    // token tiles of at most 128 where one wave of two CTAs per SM holds them, else of at
+    // most 256 (1024 tokens x 4096 x 4096 at rank 16: 38 us with tiles of 128, 45 with 256,
+    // whose epilogue no other CTA of the SM hides); smaller ones, down to 32, where the
+    // output features and the parts of the reduction leave SMs idle (3913 tokens x 78 x 64,
+    // rank 64, took 82 us on 16 CTAs of 256 tokens)
     const int64_t rtiles = cdiv(out, 128), smax = std::min<int64_t>(kI8MaxSplit, std::max<int64_t>(1, blocks / 4));
+    const int64_t widest = rtiles * cdiv(m, 128) <= 2 * sms ? 128 : 256;
     const int64_t ttiles =
-        std::max<int64_t>(cdiv(m, 256), std::min<int64_t>(cdiv(m, 32), sms / (rtiles * smax)));
+        std::max<int64_t>(cdiv(m, widest), std::min<int64_t>(cdiv(m, 32), sms / (rtiles * smax)));
     pl.sh.nt = static_cast<int>(round_up(static_cast<size_t>(cdiv(m, ttiles)), 16));
     // two CTAs per SM while their rings hold three blocks each
     const int per_sm = pl.sh.nt <= 128 ? 2 : 1;
