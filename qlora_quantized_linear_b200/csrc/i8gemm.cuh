@@ -81,10 +81,10 @@ __device__ __forceinline__ uint64_t i8_a_desc(uint32_t tile, int j) {
 // of 16 up to 256, so that a ragged batch multiplies few empty tokens.
 // HBM-bound by the weight; the ring's blocks (16 KB of weight and nt x 128
 // bytes of tokens) in flight cover the latency.  Measured: a whole call of
-// 1 token x 4096 x 4096 in 7.4 us (the weight alone is 2.6 us at the copy rate),
-// of 16 tokens x 4096 x 14336 at rank 16 in 17.6 us, where this kernel streams
+// 1 token x 4096 x 4096 in 7.3 us (the weight alone is 2.6 us at the copy rate),
+// of 16 tokens x 4096 x 14336 at rank 16 in 17.4 us, where this kernel streams
 // the 59 MB of codes at about 4.3 TB/s and the rest is the chain of three
-// launches; of 512 x 4096 x 4096 at rank 16 in 32 us.
+// launches; of 512 x 4096 x 4096 at rank 16 in 29 us.
 // ---------------------------------------------------------------------------
 constexpr int kI8SplitThreads = 192;      // producer warp, MMA warp, four epilogue warps
 constexpr int kI8MaxSplit = 8;
