@@ -152,10 +152,11 @@ __device__ __forceinline__ float absmax8(float m, const f32x2 (&v)[4]) {
 }
 
 // v times eight channel scales, one rounding to fp32 each (the input gradient
-// folds the scales into dY).
+// folds the scales into dY).  The scales are 16-byte aligned, no more: two loads.
 __device__ __forceinline__ void i8_scale8(const float* chan, f32x2 (&v)[4]) {
     f32x2 c[4];
-    asm("ld.global.nc.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(c[0]), "=l"(c[1]), "=l"(c[2]), "=l"(c[3]) : "l"(chan));
+    asm("ld.global.nc.v2.b64 {%0, %1}, [%2];" : "=l"(c[0]), "=l"(c[1]) : "l"(chan));
+    asm("ld.global.nc.v2.b64 {%0, %1}, [%2];" : "=l"(c[2]), "=l"(c[3]) : "l"(chan + 4));
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], c[e]);
 }

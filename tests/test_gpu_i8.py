@@ -240,6 +240,46 @@ def test_rows_without_values(lbq, m):
     assert lbq.device_status() == 0
 
 
+def shifted(t, count=1):
+    """A copy of t that starts `count` times 16 bytes past a 256-byte boundary."""
+    step = 16 * count // t.element_size()
+    buf = torch.empty(t.numel() + step, dtype=t.dtype, device=t.device)
+    out = buf[step:].view(t.shape)
+    out.copy_(t)
+    assert out.data_ptr() % 32 == 16 * (count % 2)
+    return out
+
+
+# every way that the row quantizer takes the channel scales: by the length of a row (pieces per thread, two passes) and
+# the number of rows, then both products and both adapter kernels
+@pytest.mark.parametrize("m,n,k,rank", [(1, 8, 16, 0), (3, 2048, 64, 8), (5, 4096, 32, 0), (5, 4104, 48, 3), (4, 8192, 32, 16),
+                                        (2, 16384, 16, 0), (2, 32768, 16, 0), (2, 40000, 16, 4), (400, 2048, 48, 0),
+                                        (300, 4096, 32, 8), (300, 8200, 16, 0), (300, 14336, 32, 16), (300, 16384, 16, 0),
+                                        (300, 28672, 16, 64), (300, 30000, 16, 0), (2600, 2000, 160, 16)])
+def test_pointers_on_16_byte_boundaries(lbq, m, n, k, rank):
+    """16 bytes is all that is asked of a pointer: every tensor of a call, the channel scales among them (a slice of one
+    buffer of scales), starts 16 bytes past a 32-byte boundary."""
+    codes, scale, A, B = layer(n, k, rank, n + k)
+    codes, scale = shifted(codes), shifted(scale)
+    A, B = (shifted(A), shifted(B)) if rank else (None, None)
+    X, dY = shifted(normal((m, k), 1.0, m)), shifted(normal((m, n), 0.1, m + 1))
+    qw = lbq.Int8Weight(n, k, codes=codes, scale=scale)
+    wf = shifted(lbq.linear_i8_fwd_workspace(m, qw, rank))
+    wb = shifted(lbq.linear_i8_bwd_workspace(m, qw, rank))
+    Y, dX = shifted(torch.zeros(m, n, device="cuda")), shifted(torch.zeros(m, k, device="cuda"))
+    T, U = (shifted(torch.zeros(m, rank, device="cuda")) for _ in range(2)) if rank else (None, None)
+    want = lbq.linear_i8_fwd(X.clone(), qw, A, B, 1.5), lbq.linear_i8_bwd(dY.clone(), qw, A, B, 1.5)
+    got = (lbq.linear_i8_fwd(X, qw, A, B, 1.5, Y=Y, T=T, workspace=wf), lbq.linear_i8_bwd(dY, qw, A, B, 1.5, dX=dX, U=U, workspace=wb))
+    for a, b in zip(want, got):
+        assert torch.equal(a[0], b[0]) and (rank == 0 or torch.equal(a[1], b[1]))
+    check_fwd(lbq, X, codes, scale, A, B, 1.5)
+    check_bwd(lbq, dY, codes, scale, A, B, 1.5)
+    W = shifted(normal((n, k), 0.02, 9, torch.float32))
+    part = lbq.Int8Weight(n, k, codes=shifted(codes), scale=shifted(scale)).quantize(W)
+    ref, rs = ref_rows(W)
+    assert torch.equal(part.codes.double(), ref) and torch.equal(part.scale, rs)
+
+
 def test_quantized_weight_round_trip(lbq):
     W = normal((300, 528), 0.02, 8)
     qw = lbq.Int8Weight(300, 528).quantize(W)
