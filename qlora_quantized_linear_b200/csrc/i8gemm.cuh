@@ -31,7 +31,9 @@ constexpr int kI8MaxReduction = 131072;   // 127^2 * 131072 < 2^31
 
 struct I8Params {
     int m, out, red;           // tokens, output features, reduction length
-    const float* row_scale;    // [m] token scales (readable up to the next multiple of 16 tokens)
+    // row_scale and T are written by kernels of the same call while this one may be resident already: they are read
+    // after griddep_wait and not through the read-only path (__ldcg); the others are complete before it starts
+    const float* row_scale;    // [m] token scales
     const float* out_scale;    // [out] channel scales, or NULL (backward)
     int rank;
     float s;
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kI8SplitThreads)
         const int64_t j = j0 + f;
         const bool ok = j < p.out;
         griddep_wait();
-        for (int t = tid; t < live; t += 128) sx[t] = __ldg(p.row_scale + t0 + t);
+        for (int t = tid; t < live; t += 128) sx[t] = __ldcg(p.row_scale + t0 + t);
         if (RP > 0) {
             const float* trow = p.T + static_cast<int64_t>(t0 + lo) * p.rank;
             constexpr int Q = RP > 0 ? RP / 4 : 1;                // 16-byte pieces of a row of sT
@@ -218,14 +220,14 @@ __global__ void __launch_bounds__(kI8SplitThreads)
                 for (int e = tid; e < (hi - lo) * Q; e += 128) {
                     const int t = e / Q, u = (e % Q) * 4;
                     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (u < p.rank) x = __ldg(reinterpret_cast<const float4*>(trow + static_cast<int64_t>(t) * p.rank + u));
+                    if (u < p.rank) x = __ldcg(reinterpret_cast<const float4*>(trow + static_cast<int64_t>(t) * p.rank + u));
                     reinterpret_cast<float4*>(sT)[e] = make_float4(p.s * x.x, p.s * x.y, p.s * x.z, p.s * x.w);
                 }
             } else {
 #pragma unroll 8
                 for (int e = tid; e < (hi - lo) * RP; e += 128) {
                     const int t = e / (RP > 0 ? RP : 1), u = e % (RP > 0 ? RP : 1);
-                    sT[e] = u < p.rank ? p.s * __ldg(trow + static_cast<int64_t>(t) * p.rank + u) : 0.0f;
+                    sT[e] = u < p.rank ? p.s * __ldcg(trow + static_cast<int64_t>(t) * p.rank + u) : 0.0f;
                 }
             }
         }
@@ -509,12 +511,12 @@ __device__ __forceinline__ void i8_stage_factors(const I8Params& p, int64_t j0, 
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (u0 + 4 * q < p.rank) x = __ldg(reinterpret_cast<const float4*>(row + 4 * q));
+                if (u0 + 4 * q < p.rank) x = __ldcg(reinterpret_cast<const float4*>(row + 4 * q));
                 v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
             }
         } else {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = (t0 + t < p.m && u0 + u < p.rank) ? __ldg(row + u) : 0.0f;
+            for (int u = 0; u < 8; ++u) v[u] = (t0 + t < p.m && u0 + u < p.rank) ? __ldcg(row + u) : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) v[u] *= p.s;
@@ -723,7 +725,7 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
             const float so = (ok && p.out_scale) ? __ldg(p.out_scale + j) : 1.0f;
             float sv[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) sv[q] = q * 32 + lane < live ? __ldg(p.row_scale + t0 + q * 32 + lane) : 0.0f;
+            for (int q = 0; q < 4; ++q) sv[q] = q * 32 + lane < live ? __ldcg(p.row_scale + t0 + q * 32 + lane) : 0.0f;
             float* row = p.Y + static_cast<int64_t>(t0) * p.out + j;
             const uint32_t taddr = tmem + static_cast<uint32_t>(buf * kI8Tile + half * 128) + (static_cast<uint32_t>(quarter * 32) << 16);
             if (!mbar_wait(&dfull[buf], (n >> 1) & 1, s_abort)) break;

@@ -152,11 +152,12 @@ __device__ __forceinline__ float absmax8(float m, const f32x2 (&v)[4]) {
 }
 
 // v times eight channel scales, one rounding to fp32 each (the input gradient
-// folds the scales into dY).  The scales are 16-byte aligned, no more: two loads.
+// folds the scales into dY).  The scales are 16-byte aligned, no more: two loads
+// (of the kind that I8Raw::load explains).
 __device__ __forceinline__ void i8_scale8(const float* chan, f32x2 (&v)[4]) {
     f32x2 c[4];
-    asm("ld.global.nc.v2.b64 {%0, %1}, [%2];" : "=l"(c[0]), "=l"(c[1]) : "l"(chan));
-    asm("ld.global.nc.v2.b64 {%0, %1}, [%2];" : "=l"(c[2]), "=l"(c[3]) : "l"(chan + 4));
+    asm volatile("ld.global.v2.b64 {%0, %1}, [%2];" : "=l"(c[0]), "=l"(c[1]) : "l"(chan));
+    asm volatile("ld.global.v2.b64 {%0, %1}, [%2];" : "=l"(c[2]), "=l"(c[3]) : "l"(chan + 4));
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], c[e]);
 }
@@ -165,11 +166,19 @@ __device__ __forceinline__ void i8_scale8(const float* chan, f32x2 (&v)[4]) {
 template <int SRC>
 struct I8Raw {
     uint4 lo, hi;          // hi: fp32 only
+    // Not the read-only path: this kernel may be resident while the one before it
+    // still writes what is read here (tokens, channel scales), and that path is
+    // for memory that does not change as long as the kernel lives.
+    static __device__ __forceinline__ uint4 load16(const uint4* p) {
+        uint4 r;
+        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+        return r;
+    }
     __device__ __forceinline__ void zero() { lo = hi = make_uint4(0u, 0u, 0u, 0u); }
     __device__ __forceinline__ void load(const void* row, int64_t j) {
         const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + j * (SRC == kSrcF32 ? 4 : 2));
-        lo = __ldg(p);
-        if (SRC == kSrcF32) hi = __ldg(p + 1);
+        lo = load16(p);
+        if (SRC == kSrcF32) hi = load16(p + 1);
     }
     __device__ __forceinline__ void values(f32x2 (&v)[4]) const {
         const uint32_t w[4] = {lo.x, lo.y, lo.z, lo.w};

@@ -378,6 +378,36 @@ def test_back_to_back_calls_and_streams(lbq):
     assert lbq.device_status() == 0
 
 
+def test_inputs_written_by_the_kernel_just_before(lbq):
+    """A kernel of this library may start while the one before it still writes: the channel scales of a weight that is
+    quantized just before its backward, and an fp32 product that is quantized itself, are the new ones every time."""
+    n, k, m = 2048, 512, 40
+    W = [normal((n, k), 0.02 * 3 ** i, 60 + i) for i in range(4)]
+    dY, X = normal((m, n), 0.1, 65), normal((m, k), 1.0, 66)
+    qw = lbq.Int8Weight(n, k)
+    Y = torch.empty(m, n, device="cuda")
+    ws = lbq.linear_i8_bwd_workspace(m, qw)
+    want = []
+    for w in W:
+        qw.quantize(w)
+        torch.cuda.synchronize()
+        dX = lbq.linear_i8_bwd(dY, qw)[0]
+        lbq.linear_i8_fwd(X, qw, Y=Y)
+        torch.cuda.synchronize()
+        want.append((dX,) + lbq.quantize_i8(Y))
+    for _ in range(10):
+        got = []
+        for w in W:
+            qw.quantize(w)
+            dX = lbq.linear_i8_bwd(dY, qw, workspace=ws)[0]
+            lbq.linear_i8_fwd(X, qw, Y=Y)
+            got.append((dX,) + lbq.quantize_i8(Y))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert lbq.device_status() == 0
+
+
 def test_temporaries_on_another_stream(lbq):
     """Calls on a stream that is not the current one, with outputs and workspaces of the helpers' own, while the
     current stream takes and writes memory too."""
