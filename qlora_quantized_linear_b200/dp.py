@@ -32,6 +32,7 @@ the multi-rank logic); there is no automatic fallback.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Callable, List, Optional, Sequence
 
 
@@ -57,7 +58,10 @@ class DataParallelQLoRA:
     torch.distributed is initialised, else a single process).
     max_grad_norm: clip the gradients of all adapters together to this
     Euclidean norm after the all-reduce (None: no clipping); `grad_norm` holds
-    the norm before, fp32 [1] on the device."""
+    the norm before, fp32 [1] on the device.
+    The methods that take a `stream` run everything on it, temporaries and
+    outputs included (None: the current stream); it may be another one than
+    that of the construction, whose fills it waits for."""
 
     def __init__(self, layers: Sequence[AdapterLayer], group=None, average: bool = False,
                  grad_fn: Optional[Callable] = None, device=None, max_grad_norm: Optional[float] = None):
@@ -82,6 +86,29 @@ class DataParallelQLoRA:
         if self.max_grad_norm is not None:
             from . import lbq
             self._clip = lbq.GradClip([self.flat])
+        self._ordered = set()              # streams whose work comes after the fill of the flat buffer
+        if self.flat.is_cuda:
+            here = torch.cuda.current_stream(self.flat.device)
+            self._ordered.add(here.cuda_stream)
+            self._filled = None if torch.cuda.is_current_stream_capturing() else here.record_event()
+
+    def _on(self, stream):
+        """Makes `stream` (None: the current one) the current stream of a part
+        of the step, after the fill of the flat buffer.  (A stream that is
+        being captured cannot wait for work outside its graph; torch.cuda.graph
+        waits for the device when it begins.)"""
+        if not self.flat.is_cuda:
+            return contextlib.nullcontext()
+        cuda = self.torch.cuda
+        if stream is None:
+            stream = cuda.current_stream(self.flat.device)
+        if stream.cuda_stream not in self._ordered:
+            with cuda.stream(stream):
+                if self._filled is not None and not cuda.is_current_stream_capturing():
+                    stream.wait_event(self._filled)
+                    self.flat.record_stream(stream)
+                    self._ordered.add(stream.cuda_stream)
+        return cuda.stream(stream)
 
     # ------------------------------------------------------------------ ranks
     def _dist(self):
@@ -99,19 +126,20 @@ class DataParallelQLoRA:
         [m_r, n_i].  Writes the rank's dA, dB into the flat buffer and returns
         [(Y_r, dX_r)] per layer."""
         outs = []
-        for L, (X, dY) in zip(self.layers, shards):
-            if self.grad_fn is not None:
-                Y, dX, dA, dB = self.grad_fn(L, X, dY)
-                L.dA.copy_(dA)
-                L.dB.copy_(dB)
-            else:
-                from . import lbq
-                i8 = isinstance(L.qw, lbq.Int8Weight)
-                fwd, bwd = (lbq.linear_i8_fwd, lbq.linear_i8_bwd) if i8 else (lbq.linear_fwd, lbq.linear_bwd)
-                Y, T = fwd(X, L.qw, L.A, L.B, L.s, stream=stream)
-                dX, U = bwd(dY, L.qw, L.A, L.B, L.s, stream=stream)
-                lbq.lora_grads(X, dY, T, U, L.s, dA=L.dA, dB=L.dB, stream=stream)
-            outs.append((Y, dX))
+        with self._on(stream):
+            for L, (X, dY) in zip(self.layers, shards):
+                if self.grad_fn is not None:
+                    Y, dX, dA, dB = self.grad_fn(L, X, dY)
+                    L.dA.copy_(dA)
+                    L.dB.copy_(dB)
+                else:
+                    from . import lbq
+                    i8 = isinstance(L.qw, lbq.Int8Weight)
+                    fwd, bwd = (lbq.linear_i8_fwd, lbq.linear_i8_bwd) if i8 else (lbq.linear_fwd, lbq.linear_bwd)
+                    Y, T = fwd(X, L.qw, L.A, L.B, L.s)
+                    dX, U = bwd(dY, L.qw, L.A, L.B, L.s)
+                    lbq.lora_grads(X, dY, T, U, L.s, dA=L.dA, dB=L.dB)
+                outs.append((Y, dX))
         return outs
 
     def all_reduce(self, stream=None):
@@ -123,12 +151,7 @@ class DataParallelQLoRA:
             if self.average:
                 pass                                   # one rank: its mean is the mean
             return
-        if stream is not None and self.flat.is_cuda:
-            with self.torch.cuda.stream(stream):
-                d.all_reduce(self.flat, op=d.ReduceOp.SUM, group=self.group)
-                if self.average:
-                    self.flat.div_(d.get_world_size(self.group))
-        else:
+        with self._on(stream):
             d.all_reduce(self.flat, op=d.ReduceOp.SUM, group=self.group)
             if self.average:
                 self.flat.div_(d.get_world_size(self.group))
@@ -137,7 +160,8 @@ class DataParallelQLoRA:
         """Clip the adapters' gradients to max_grad_norm (nothing without one);
         after the all-reduce, on the same stream."""
         if self.max_grad_norm is not None:
-            self.grad_norm = self._clip.clip(self.max_grad_norm, stream=stream)
+            with self._on(stream):
+                self.grad_norm = self._clip.clip(self.max_grad_norm)
 
     def step(self, shards, stream=None):
         """local_step, all_reduce, clip; returns the per-layer (Y_r, dX_r)."""

@@ -661,9 +661,12 @@ class GradClip:
     the workspace.  `grads` are contiguous fp32, bf16 or fp16 CUDA tensors; `outs` (default: the gradients
     themselves) get the scaled copies, with the same types and sizes.  The tensors are held, so their memory
     stays theirs; calls of one GradClip that may run at the same time race on its workspace, which is zeroed on
-    the stream that is current here: a call on another stream has to come after that."""
+    the stream that is current here: the first call on another stream waits for that.  (Not a call that is being
+    captured, which cannot wait for work outside its graph: `torch.cuda.graph` waits for the device when it begins,
+    and so has to whoever begins a capture by hand before the workspace is zeroed.  A plan made inside a capture is
+    that graph's alone.)"""
 
-    def __init__(self, grads, outs=None):
+    def __init__(self, grads, outs=None, *, _one_call=False):
         torch = _torch()
         self.grads = list(grads)
         self.outs = self.grads if outs is None else list(outs)
@@ -686,12 +689,34 @@ class GradClip:
             raise ValueError("the gradients must be CUDA tensors")
         self.total_norm = torch.empty(1, dtype=torch.float32, device=dev)
         self.workspace = torch.zeros(lbq_grad_norm_workspace_size(len(self.grads)), dtype=torch.uint8, device=dev)
+        # streams whose work comes after the zero fill, and what others wait for (an event takes 6 us: not where the
+        # only call follows here)
+        self._ordered = {torch._C._cuda_getCurrentRawStream(dev.index)}
+        self._zeroed = None
+        if not _one_call and not torch.cuda.is_current_stream_capturing():
+            self._zeroed = torch.cuda.current_stream(dev).record_event()
+
+    def _order(self, stream):
+        """Puts a stream's work after the workspace's zero fill, which another stream was given."""
+        torch = _torch()
+        if stream is None:
+            stream = torch.cuda.current_stream(self.total_norm.device)
+        with torch.cuda.stream(stream):
+            if self._zeroed is None or torch.cuda.is_current_stream_capturing():
+                return
+            stream.wait_event(self._zeroed)
+            for t in (self.total_norm, self.workspace):      # their memory is not reused before this stream is done
+                t.record_stream(stream)
+        self._ordered.add(stream.cuda_stream)
 
     def norm(self, stream=None):
         """The Euclidean norm of all gradients together (fp32 [1], on the device)."""
         _same_device(self.total_norm.device)
+        st = _stream(stream)
+        if st not in self._ordered:
+            self._order(stream)
         _check(lbq_grad_norm(self.table, len(self.grads), self.total_norm.data_ptr(), self.workspace.data_ptr(),
-                             self.workspace.numel(), _stream(stream)), "lbq_grad_norm")
+                             self.workspace.numel(), st), "lbq_grad_norm")
         return self.total_norm
 
     def clip(self, max_norm: float, stream=None):
@@ -701,6 +726,8 @@ class GradClip:
         if dev != torch._C._cuda_getDevice():
             raise ValueError(f"the gradients are on cuda:{dev}, not on the current CUDA device")
         st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+        if st not in self._ordered:
+            self._order(stream)
         _check(lbq_clip_grad_norm(self.table, len(self.grads), max_norm, self.total_norm.data_ptr(),
                                   self.workspace.data_ptr(), self.workspace.nbytes, st), "lbq_clip_grad_norm")
         return self.total_norm
@@ -709,13 +736,13 @@ class GradClip:
 def grad_norm(grads, stream=None):
     """The Euclidean norm of all `grads` together (fp32 [1], on the device)."""
     with _on(stream):
-        return GradClip(grads).norm()
+        return GradClip(grads, _one_call=True).norm()
 
 
 def clip_grad_norm(grads, max_norm: float, outs=None, stream=None):
     """Clip `grads` to max_norm, in place or into `outs`; returns their norm before (fp32 [1], on the device)."""
     with _on(stream):
-        return GradClip(grads, outs).clip(max_norm)
+        return GradClip(grads, outs, _one_call=True).clip(max_norm)
 
 
 def device_status() -> int:

@@ -261,3 +261,58 @@ def test_some_in_place_some_not_and_nothing_to_clip(lbq):
     for g, o, b in zip(grads, outs, before):
         assert torch.equal(g, b) and torch.equal(o, b)
     assert lbq.device_status() == 0
+
+
+def test_a_plan_made_behind_queued_work_and_used_on_another_stream(lbq):
+    """The plan's workspace is zeroed on the stream of its construction, which is milliseconds behind: the first call on
+    another stream, clip or norm, waits for that, and the workspace is not given away under it."""
+    grads = [normal(n, 0.5, n) for n in (300_001, 33, 4096)]
+    want = ref_norm(grads)
+    coef = 1.0 / (want + 1e-6)
+    big = normal(1 << 26, 1.0, 1)
+    for use in ("clip", "norm"):
+        for _ in range(5):
+            copies = [g.clone() for g in grads]
+            dirt = [torch.full((1 << 12,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(64)]
+            side = torch.cuda.Stream()
+            torch.cuda.synchronize()
+            for _ in range(20):
+                big.mul_(1.0001)
+            del dirt
+            plan = lbq.GradClip(copies)
+            norm = plan.clip(1.0, stream=side) if use == "clip" else plan.norm(stream=side)
+            again = plan.norm(stream=side).clone() if use == "norm" else None
+            del plan
+            rewrite = [torch.full((1 << 12,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(64)]
+            torch.cuda.synchronize()
+            assert lbq.device_status() == 0
+            assert norm_is(norm.item(), want) and len(rewrite) == 64
+            if use == "norm":
+                assert all(torch.equal(g, c) for g, c in zip(grads, copies)) and again.numel() == 1
+            else:
+                for g, c in zip(grads, copies):
+                    assert bool(((c.double() - g.double() * coef).abs() <= 7 * STEP * g.double().abs() * coef).all())
+
+
+def test_a_plan_in_a_graph_before_any_other_call(lbq):
+    """Captured at its first use, then replayed, then called on the stream of its construction and on a third one."""
+    grads = [normal(n, 0.5, n) for n in (70_001, 12)]
+    outs = [torch.empty_like(g) for g in grads]
+    plan = lbq.GradClip(grads, outs)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        plan.clip(0.25)
+    g.replay()
+    torch.cuda.synchronize()
+    want = ref_norm(grads)
+    assert norm_is(plan.total_norm.item(), want)
+    first = [o.clone() for o in outs]
+    side = torch.cuda.Stream()
+    for stream in (None, side, side, None):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        assert norm_is(plan.clip(0.25, stream=stream).item(), want)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, first))
+    assert lbq.device_status() == 0

@@ -481,3 +481,34 @@ def test_training_step_with_clipping(lbq):
     loose.step(shards)
     assert torch.equal(loose.flat, raw)
     assert lbq.device_status() == 0
+
+
+@pytest.mark.parametrize("eight", [True, False])
+def test_training_step_on_a_side_stream(lbq, eight):
+    """A step built behind queued work and run on another stream at once: the flat buffer, the clipping's workspace and
+    every temporary are filled in that stream's order.  Same bits as on the current stream."""
+    from qlora_quantized_linear_b200.dp import AdapterLayer, DataParallelQLoRA
+    m, s = 24, 2.0
+    layers, shards = [], []
+    for i, (n, k, r) in enumerate([(256, 512, 8), (384, 1024, 16)]):
+        W = normal((n, k), 0.02, 50 + i)
+        qw = lbq.Int8Weight(n, k).quantize(W) if eight else lbq.QuantizedWeight(n, k, "minmax", 4).quantize(W)
+        layers.append(AdapterLayer(qw, normal((r, k), 0.01, 60 + i), normal((n, r), 0.01, 70 + i), s))
+        shards.append((normal((m, k), 1.0, 80 + i), normal((m, n), 0.1, 90 + i)))
+    plain = DataParallelQLoRA(layers, max_grad_norm=0.5)
+    want = [t.clone() for pair in plain.step(shards) for t in pair] + [plain.flat.clone(), plain.grad_norm.clone()]
+    big = normal((1 << 26,), 1.0, 1, torch.float32)
+    for _ in range(3):
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        dirt = [torch.full((1 << i,), 0x5A, dtype=torch.uint8, device="cuda") for i in range(8, 20) for _ in range(4)]
+        for _ in range(20):
+            big.mul_(1.0001)
+        del dirt
+        step = DataParallelQLoRA(layers, max_grad_norm=0.5)
+        outs = step.step(shards, stream=side)
+        torch.cuda.synchronize()
+        got = [t for pair in outs for t in pair] + [step.flat, step.grad_norm]
+        assert lbq.device_status() == 0
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
