@@ -8,9 +8,11 @@
 // warps take 16 of each chunk's 128 steps, so a fragment of the adapter's
 // factor serves all the CTA's tokens.  The products run on mma.sync (bf16 in,
 // fp32 sums); the parts of a token tile form a cluster and are joined over
-// distributed shared memory in a fixed order.  A warp's chain of sums is
-// len / (128 parts) long, which keeps T near the accuracy of an fp32 tree: the
-// adapter's term enters the output in fp32.
+// distributed shared memory in a fixed order.  A warp's sum takes one product of
+// 16 terms per chunk and is kept in fp32 registers outside the tensor core, whose
+// own additions truncate: U over 28672 at rank 33 for 2048 tokens was off by
+// 8.6e-7 rms with chains of them and is by 1.5e-7 (an fp32 product: 3.0e-7), for
+// 84 us instead of 75 at 4096 x 14336, rank 36.
 #pragma once
 
 #include "common.cuh"
@@ -96,6 +98,7 @@ __global__ void __launch_bounds__(kAdThreads) i8_adapter_kernel(const uint16_t* 
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
+    // a product of 16 terms by the tensor core, its addition to the sum in fp32: a tensor core's own would truncate
     float acc[TILES][R8][4];
 #pragma unroll
     for (int i = 0; i < TILES; ++i)
@@ -154,7 +157,12 @@ __global__ void __launch_bounds__(kAdThreads) i8_adapter_kernel(const uint16_t* 
             uint32_t a[4];
             ldmatrix_x4(a, sx + (mt * 16 + (q & 1) * 8 + l8) * L::kRow + (kk + (q >> 1) * 8) * 2);
 #pragma unroll
-            for (int t = 0; t < R8; ++t) lora_mma(acc[mt][t], a[0], a[1], a[2], a[3], b[t][0], b[t][1]);
+            for (int t = 0; t < R8; ++t) {
+                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                lora_mma(d, a[0], a[1], a[2], a[3], b[t][0], b[t][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[mt][t][e] += d[e];
+            }
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -203,8 +211,12 @@ __global__ void __launch_bounds__(kAdThreads) i8_adapter_kernel(const uint16_t* 
 // K-major A operand, the adapter's factor as the B operand, K-major in the
 // forward and MN-major (the rank contiguous) in the backward, where its rows of
 // 2 r bytes need a multiple of 16 (r % 8 == 0; other ranks take the kernel
-// above).  The MMAs of a block go to several accumulators in turn, which the
-// epilogue adds in fp32: chains of sums in tensor memory stay short.
+// above).  A tensor core's addition to its accumulator truncates, so chains of
+// them stay short: the blocks go to the accumulators of a bank in turn, four
+// blocks (16 MMAs) each, while the epilogue warps add the other bank's to fp32
+// registers, whose additions round.  (U of 2048 tokens x 28672 at rank 64: off by
+// 1.2e-6 rms with chains of 75 MMAs and by 2.5e-7 so, an fp32 product by 3.0e-7;
+// 38 us instead of 36.)
 // HBM-bound: 4096 tokens x 14336 at rank 16 in 28 us (4.2 TB/s, 0.64 of the copy
 // rate), x 4096 in 15 us from cold caches (2.3 TB/s: the start, four rounds of
 // the ring and the join are of one size).
@@ -221,10 +233,11 @@ struct AdapterTcSmem {
     static constexpr int kXBytes = 128 * 128;
     static constexpr int kWBytes = NR * 128;
     static constexpr int kStageBytes = kXBytes + kWBytes;
-    static constexpr int kSets = 256 / NR;                     // accumulators of NR columns
+    static constexpr int kSets = 128 / NR;                     // accumulators of NR columns in each of two banks
+    static constexpr int kRound = 4 * kSets;                   // blocks to a bank before it is drained
     static constexpr int kRow = NR + 1;                        // the sums of a token, read by the cluster
     static constexpr size_t kBar = size_t(kStages) * kStageBytes;
-    static constexpr size_t kBytes = kBar + (2 * kStages + 1) * 8 + 16 + 1024;
+    static constexpr size_t kBytes = kBar + (2 * kStages + 5) * 8 + 16 + 1024;
     static_assert(size_t(128) * kRow * 4 <= kBar, "the sums reuse the ring");
 };
 
@@ -248,8 +261,10 @@ __global__ void __launch_bounds__(kAdTcThreads) i8_adapter_tc_kernel(const __gri
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
     uint64_t* empty = full + S;
-    uint64_t* dfull = empty + S;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(dfull + 1);
+    uint64_t* dfull = empty + S;        // a bank's sums are complete
+    uint64_t* dempty = dfull + 2;       // a bank is drained
+    uint64_t* done = dempty + 2;        // every MMA is
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = static_cast<int>(gridDim.y), part = static_cast<int>(blockIdx.y);
@@ -262,7 +277,11 @@ __global__ void __launch_bounds__(kAdTcThreads) i8_adapter_tc_kernel(const __gri
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        mbar_init(dfull, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dempty[i], 4);   // four epilogue warps
+        }
+        mbar_init(done, 1);
         *s_abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmX);
@@ -294,43 +313,68 @@ __global__ void __launch_bounds__(kAdTcThreads) i8_adapter_tc_kernel(const __gri
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            for (int i = 0; i < nb; ++i) {
-                const int st = i % S;
-                if (!mbar_wait(&full[st], (i / S) & 1, s_abort)) break;
-                tc_fence_after();
-                const uint32_t x = smem_u32(smem + st * L::kStageBytes), w = x + L::kXBytes;
-                const uint32_t d = tmem + static_cast<uint32_t>((i % L::kSets) * NR);
+            // (a loop of rounds: a commit under a condition in the loop of blocks cost 2 us of 36)
+            int st = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int i0 = 0, rd = 0; ok && i0 < nb; i0 += L::kRound, ++rd) {
+                if (rd >= 2 && !mbar_wait(&dempty[rd & 1], ((rd >> 1) - 1) & 1, s_abort)) break;
+                const uint32_t bank = tmem + static_cast<uint32_t>((rd & 1) * 128);
+                const int n = min(nb - i0, L::kRound);
+                for (int c = 0; c < n; ++c) {
+                    ok = mbar_wait(&full[st], ph, s_abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t x = smem_u32(smem + st * L::kStageBytes), w = x + L::kXBytes;
+                    const uint32_t d = bank + static_cast<uint32_t>((c % L::kSets) * NR);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    mma_ss(d, smem_desc_k_sw128(x) + static_cast<uint64_t>(2 * j),
-                           COL ? smem_desc_mn_rank<NR>(w + j * 32 * NR) : smem_desc_k_sw128(w) + static_cast<uint64_t>(2 * j),
-                           kIdesc, (i >= L::kSets || j > 0) ? 1u : 0u);
-                mma_commit(&empty[st]);
+                    for (int j = 0; j < 4; ++j)
+                        mma_ss(d, smem_desc_k_sw128(x) + static_cast<uint64_t>(2 * j),
+                               COL ? smem_desc_mn_rank<NR>(w + j * 32 * NR)
+                                   : smem_desc_k_sw128(w) + static_cast<uint64_t>(2 * j),
+                               kIdesc, (c >= L::kSets || j > 0) ? 1u : 0u);
+                    mma_commit(&empty[st]);
+                    if (++st == S) st = 0, ph ^= 1u;
+                }
+                if (ok) mma_commit(&dfull[rd & 1]);
             }
-            mma_commit(dfull);
-            mbar_wait_drain(dfull, 0);
+            mma_commit(done);
+            mbar_wait_drain(done, 0);
         }
     } else {
         const int quarter = warp & 3, row = quarter * 32 + lane;
-        const bool done = mbar_wait(dfull, 0, s_abort);
-        tc_fence_after();
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        float* sum = reinterpret_cast<float*>(smem) + row * L::kRow;
-        const int sets = min(nb, L::kSets);
+        float v[NR];
+#pragma unroll
+        for (int e = 0; e < NR; ++e) v[e] = 0.0f;
+        const int rounds = (nb + L::kRound - 1) / L::kRound;
+        bool ok = true;
 #pragma unroll 1
-        for (int c = 0; done && c < NR; c += 16) {
-            float v[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = 0.0f;
+        for (int rd = 0; rd < rounds; ++rd) {
+            const int bank = rd & 1, sets = min(nb - rd * L::kRound, L::kSets);
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(&dfull[bank], (rd >> 1) & 1, s_abort));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
             for (int k = 0; k < sets; ++k) {
-                uint32_t a[16];
-                tmem_ld_32x32b_x16(taddr + k * NR + c, a);
-                tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(a[e]);
+                for (int c = 0; c < NR; c += 16) {
+                    uint32_t a[16];
+                    tmem_ld_32x32b_x16(taddr + bank * 128 + k * NR + c, a);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[c + e] += __uint_as_float(a[e]);
+                }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&dempty[bank]);
+        }
+        // the last bank is complete, so is every block before it: the ring is free
+        if (ok) {
+            float* sum = reinterpret_cast<float*>(smem) + row * L::kRow;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) sum[c + e] = v[e];
+            for (int e = 0; e < NR; ++e) sum[e] = v[e];
         }
     }
     tc_fence_before();

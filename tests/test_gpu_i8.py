@@ -219,6 +219,29 @@ def test_largest_sums_do_not_wrap(lbq):
     assert dX[0, 0] > 0 and dX[1, 0] < 0
 
 
+@pytest.mark.parametrize("m", [5, 17, 130])
+@pytest.mark.parametrize("rank", [3, 8, 16, 32, 33, 64])
+def test_adapter_product_keeps_small_terms(lbq, m, rank):
+    """A one and then 131071 products of 1.75 * 2^-28: sixteen of them are 7/8 of a step of fp32 at the sum, so a chain of
+    tensor-core additions (a product of 16 terms each, truncated) loses as many steps as it is long after the one.  At
+    most 16 such additions follow one another before the sum is taken to fp32 registers.  There every addition onto the
+    one is off by half a step at most, and there are at most 144: 128 of a warp's products or 64 of a CTA's chains (the
+    reduction is in 8 parts), 8 of the warps and 8 of the parts.  In all 16 + 72 steps of 2^-23."""
+    red = 131072
+    small = 1.75 * 2.0 ** -28
+    P = torch.full((rank, red), small, device="cuda").to(torch.bfloat16)
+    P[:, 0] = 1.0
+    ones = torch.ones((m, red), device="cuda", dtype=torch.bfloat16)
+    want, lim = 1.0 + (red - 1) * small, (16 + 72) * 2.0 ** -23
+    other = torch.zeros((16, rank), device="cuda", dtype=torch.bfloat16)
+    codes = torch.ones((16, red), dtype=torch.int8, device="cuda")
+    T = lbq.linear_i8_fwd(ones, lbq.Int8Weight(16, red, codes=codes, scale=torch.ones(16, device="cuda")), P, other, 1.0)[1]
+    assert (T.double() - want).abs().max().item() <= lim
+    U = lbq.linear_i8_bwd(ones, lbq.Int8Weight(red, 16, codes=codes.t().contiguous(), scale=torch.ones(red, device="cuda")),
+                          other.t().contiguous(), P.t().contiguous(), 1.0)[1]
+    assert (U.double() - want).abs().max().item() <= lim
+
+
 @pytest.mark.parametrize("m", [6, 40, 2600])
 def test_rows_without_values(lbq, m):
     """Zero tokens give zeros (plus the adapter's zero); a token with an infinity or a NaN gives NaN and leaves the
