@@ -168,10 +168,12 @@ struct I8Raw {
     uint4 lo, hi;          // hi: fp32 only
     // Not the read-only path: this kernel may be resident while the one before it
     // still writes what is read here (tokens, channel scales), and that path is
-    // for memory that does not change as long as the kernel lives.
+    // for memory that does not change as long as the kernel lives.  L1 is left to
+    // the channel scales, which the CTAs of an SM share (4096 x 14336 scaled rows:
+    // 44.7 us, 45.4 without the hint).
     static __device__ __forceinline__ uint4 load16(const uint4* p) {
         uint4 r;
-        asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
         return r;
     }
     __device__ __forceinline__ void zero() { lo = hi = make_uint4(0u, 0u, 0u, 0u); }
