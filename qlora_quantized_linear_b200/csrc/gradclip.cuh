@@ -41,7 +41,7 @@ constexpr int kClipVecs = 4;                          // 16-byte pieces per lane
 constexpr int kClipChunk = kClipVecs * 32 * 16;       // 2 KB
 constexpr int kClipSlots = 6;                         // chunks of a warp's ring
 constexpr int kClipRing = kClipWarps * kClipSlots * kClipChunk;
-constexpr uint32_t kClipL2 = 80u << 20;               // bytes of a launch that are held in L2 between the phases
+constexpr uint32_t kClipL2 = 80u << 20;               // bytes of a launch that L2 is asked to hold between the phases
 constexpr int kClipMaxCtas = 256;                     // CTAs of a launch
 constexpr int kClipTable = 976;                       // tensors per launch (kernel arguments are below 32764 bytes)
 
@@ -179,8 +179,13 @@ __device__ __forceinline__ void grad_scale_of(uint4 (&r)[4], int type, float c) 
     else grad_scale<kGradF16>(r, c);
 }
 
-// L2 eviction policies: pieces that are read again in the same launch stay as
-// long as they can, what is not needed again makes room first.
+// L2 eviction policies: the gradients of the last kClipL2 bytes stay as long as
+// they can, the other gradients and the outputs make room first.  The scaling's
+// own reads keep the first read's policy, although nothing reads them a third
+// time: with evict_first there 20 M fp32 values took 62 us instead of 57 and 168 M
+// bf16 values 200 instead of 197, and what runs next was no faster for it (five
+// passes over another 96 MB: 85 us after either, 88 with an empty L2; a read of
+// the outputs: 45 us after 42 M values, 24.5 after 20 M).
 __device__ __forceinline__ uint64_t l2_policy(bool last) {
     uint64_t p;
     if (last) asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
