@@ -1,8 +1,10 @@
 """The gradient norm and clipping on the GPU against fp64.
 
-The squares of a 16-byte piece (at most 8) are added in fp32: at most 8 steps
-of 2^-24 off, all sums after that in fp64.  The norm's square root halves the
-relative error and the result is rounded once: 5 * 2^-24 bounds it.  An output
+The squares of a lane's four 16-byte pieces are added in fp32: chains of four
+(4 roundings), the two halves of a 16-bit piece (1), the pieces in pairs (2), so
+at most 7 roundings of 2^-24; all sums after that are in fp64.  The norm's square
+root halves the relative error and the result is rounded once: 4.5 * 2^-24, and
+5 * 2^-24 bounds it.  An output
 is the fp32 product of the value with a coefficient that is off by as much and
 rounded once (7 * 2^-24 in all), then rounded to its type.
 """
