@@ -55,19 +55,20 @@ lbq_status launch_overlapped(dim3 grid, int threads, size_t smem, dim3 cluster, 
     return LBQ_OK;
 }
 
-// How many clusters of `parts` CTAs (at most 8) run at the same time, per_sm (1
-// or 2) CTAs to an SM: a cluster stays within a group of SMs, and the groups
-// are of several sizes, so clusters leave SMs over.  (Sixteen clusters of 8 do not
-// fit one CTA per SM: the adapter product of 2048 tokens x 28672 at rank 16 took
-// two waves, 55 us, and takes one of 16 clusters of 6, 36 us.)  Asked once per
-// device, for a kernel of no tensor memory with that much shared memory: the
-// answer for one that has it counted a single CTA per SM.
+// How many clusters of `parts` CTAs (at most 16; 0 of more than 8 where no group
+// of SMs has room for one) run at the same time, per_sm (1 or 2) CTAs to an SM: a
+// cluster stays within a group of SMs, and the groups are of several sizes, so
+// clusters leave SMs over.  (Sixteen clusters of 8 do not fit one CTA per SM: the
+// adapter product of 2048 tokens x 28672 at rank 16 took two waves, 55 us, and
+// takes one of 16 clusters of 6, 36 us.)  Asked once per device, for a kernel of
+// no tensor memory with that much shared memory: the answer for one that has it
+// counted a single CTA per SM.
 int clusters_that_fit(int parts, int per_sm, int sms) {
-    static std::atomic<int> known[16][2][kI8MaxSplit + 1];
+    static std::atomic<int> known[16][2][kAdMaxParts + 1];      // one more than the answer, 0 until it is asked
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return per_sm * sms / parts;
     std::atomic<int>* slot = dev < 16 ? &known[dev][per_sm - 1][parts] : nullptr;
-    if (slot && (n = slot->load(std::memory_order_relaxed)) > 0) return n;
+    if (slot && (n = slot->load(std::memory_order_relaxed)) > 0) return n - 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, static_cast<unsigned>(parts));
     cfg.blockDim = dim3(256);
@@ -79,11 +80,12 @@ int clusters_that_fit(int parts, int per_sm, int sms) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     constexpr auto kern = i8_quantize_rows_kernel<kSrcBf16, false, false, 1, 256>;
-    if (!raise_limits<kern>(dev) || cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-        (void)cudaGetLastError();
-        n = per_sm * sms / parts;
-    }
-    if (slot) slot->store(n, std::memory_order_relaxed);
+    const bool asked = raise_limits<kern>(dev) && cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess;
+    if (!asked) (void)cudaGetLastError();
+    // clusters of 8 are portable: any GPU runs one
+    if (parts > 8) n = asked ? n : 0;
+    else if (!asked || n < 1) n = std::max(1, per_sm * sms / parts);
+    if (slot) slot->store(n + 1, std::memory_order_relaxed);
     return n;
 }
 
@@ -139,11 +141,11 @@ lbq_status run_i8_quantize(const void* in, int64_t rows, int64_t len, const floa
 template <bool COL, int MT, int R8>
 lbq_status launch_i8_adapter(const void* in, int64_t m, int64_t len, const void* wt, int r, float* out, int sms,
                              cudaStream_t st) {
-    // one token tile: as many parts as a cluster holds; more: parts that fill the SMs
+    // one token tile: as many parts as a cluster holds on this GPU; more: parts that fill the SMs
     const int64_t groups = cdiv(m, MT), chunks = cdiv(len, kAdChunk);
     constexpr int kPerSm = AdapterSmem<MT, R8>::kBytes <= 106 * 1024 ? 2 : 1;
     const int64_t parts =
-        MT <= 16 ? std::min<int64_t>(kAdMaxParts, chunks)
+        MT <= 16 ? parts_that_fit(std::min<int64_t>(kAdMaxParts, chunks), 1, 1, sms)
                  : parts_that_fit(std::min<int64_t>({8, chunks, std::max<int64_t>(1, kPerSm * sms / groups)}), groups, kPerSm, sms);
     return launch_overlapped<i8_adapter_kernel<COL, MT, R8>>(
         dim3(static_cast<unsigned>(groups), static_cast<unsigned>(parts)), kAdThreads, AdapterSmem<MT, R8>::kBytes,
