@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kI8PairThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = blockIdx.x & 1u;
     const int jtiles = (p.out + kI8Tile - 1) / kI8Tile;
-    const int tiles = jtiles * ((p.m + kI8Tile - 1) / kI8Tile);
+    const int tiles = jtiles * ((p.m - 1) / kI8Tile + 1);      // any m up to 2^31 - 1: nothing is added to it
     const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
     const int nb = (p.red + 127) / 128;
 
