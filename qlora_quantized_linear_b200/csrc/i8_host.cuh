@@ -195,8 +195,10 @@ template <bool BWD>
 lbq_status run_i8_factor(const void* in, int64_t m, int64_t len, const void* wt, int r, float* out, int sms,
                          cudaStream_t st) {
     if (m <= 16) return run_i8_adapter<BWD, 16>(in, m, len, wt, r, out, sms, st);
-    if (!BWD || r % 8 == 0) return run_i8_adapter_tc<BWD>(in, m, len, wt, r, out, sms, st);
-    return run_i8_adapter<BWD, 64>(in, m, len, wt, r, out, sms, st);
+    if constexpr (BWD) {
+        if (r % 8 != 0) return run_i8_adapter<true, 64>(in, m, len, wt, r, out, sms, st);
+    }
+    return run_i8_adapter_tc<BWD>(in, m, len, wt, r, out, sms, st);
 }
 
 // ---------------------------------------------------------------------------
