@@ -101,6 +101,8 @@ class DataParallelQLoRA:
             return contextlib.nullcontext()
         cuda = self.torch.cuda
         if stream is None:
+            if self.torch._C._cuda_getCurrentRawStream(self.flat.device.index) in self._ordered:
+                return contextlib.nullcontext()
             stream = cuda.current_stream(self.flat.device)
         if stream.cuda_stream not in self._ordered:
             with cuda.stream(stream):
