@@ -83,10 +83,10 @@ __device__ __forceinline__ uint64_t i8_a_desc(uint32_t tile, int j) {
 // of 16 up to 256, so that a ragged batch multiplies few empty tokens.
 // HBM-bound by the weight; the ring's blocks (16 KB of weight and nt x 128
 // bytes of tokens) in flight cover the latency.  Measured: a whole call of
-// 1 token x 4096 x 4096 in 7.3 us (the weight alone is 2.6 us at the copy rate),
-// of 16 tokens x 4096 x 14336 at rank 16 in 17.4 us, where this kernel streams
+// 1 token x 4096 x 4096 in 8.2 us (the weight alone is 2.6 us at the copy rate),
+// of 16 tokens x 4096 x 14336 at rank 16 in 18.5 us, where this kernel streams
 // the 59 MB of codes at about 4.3 TB/s and the rest is the chain of three
-// launches; of 512 x 4096 x 4096 at rank 16 in 29 us.
+// launches, both with L2 flushed before the call; of 512 x 4096 x 4096 at rank 16 in 29 us.
 // ---------------------------------------------------------------------------
 constexpr int kI8SplitThreads = 192;      // producer warp, MMA warp, four epilogue warps
 constexpr int kI8MaxSplit = 8;
@@ -378,7 +378,9 @@ __global__ void __launch_bounds__(kI8SplitThreads)
 // Measured at 4096 tokens, rank 16: forward to 14336 features from 4096 198 us
 // (2.43 P operations/s; 235 MB of output: its stores cost about 23 us), backward
 // to 4096 features from 14336 179 us (2.69 P).  MMAs alone run at 2.9 to 3.1 P at the
-// clock that the power limit leaves (about 1.65 GHz), loads alone at 2.8 P.
+// clock that the power limit leaves (about 1.65 GHz), loads alone at 2.8 P.  With
+// an adapter an epilogue thread holds 128 sums while the term is formed and spills
+// 96 bytes of its 168 registers' worth.
 // ---------------------------------------------------------------------------
 constexpr int kI8PairThreads = 320;       // producer warp, MMA warp, eight epilogue warps
 constexpr int kI8Tile = 256;              // output features and tokens of a pair's tile

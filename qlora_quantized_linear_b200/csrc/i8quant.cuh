@@ -205,8 +205,9 @@ struct I8Raw {
 // as they were stored, or scaled) between its maximum and its codes, or is read
 // twice (NV == 0).  Many rows keep 64 to 112 bytes a thread in flight with up to
 // 1024 threads per SM (4096 x 14336 bf16: 28 us, 0.96 of the copy rate; with
-// channel scales 43 us, bound by reading them and by the exact check); few rows
-// take as many threads as the row has pieces.  len % 8 == 0.
+// channel scales 45 us, bound by reading them and by the exact check, with 64 of
+// a thread's bytes spilled at seven pieces); few rows take as many threads as the
+// row has pieces.  len % 8 == 0.
 // BESIDE: the kernel before this one (the adapter's product of the same call)
 // started after everything before it was complete and touches nothing of this
 // one's, so the two run side by side; waiting for it comes last, so that the
