@@ -494,8 +494,9 @@ lbq_status lbq_quantize_i8(const void* X, int dtype, int rows, int k, int8_t* co
  *   Y[t, j] = fp32(sum_i Xq[t, i] codes[j, i]) sx[t] scale[j] + s sum_u T[t, u] B[j, u]   (fp32)
  * The sum of 8-bit products is exact (int32), so Y does not depend on how the
  * work is split; the two scales are multiplied in the order written, and the
- * adapter's term is computed from fp32(s T) in fp32.  X bf16 [m, k], A bf16 [rank, k], B bf16
- * [n, rank], T_save fp32 [m, rank], Y fp32 [m, n], all row-major device.
+ * adapter's term is computed from fp32(s T) in fp32 (an infinite element of a
+ * factor makes what it enters infinite or NaN).  X bf16 [m, k], A bf16 [rank, k],
+ * B bf16 [n, rank], T_save fp32 [m, rank], Y fp32 [m, n], all row-major device.
  * rank == 0 (A, B, T_save may be NULL) has no adapter; 0 <= rank <= 64.
  * m >= 1; any n.  workspace: lbq_linear_i8_fwd_workspace_size bytes of device
  * memory with any contents (the tokens' codes and scales); calls that may run

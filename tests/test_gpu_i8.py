@@ -303,6 +303,25 @@ def test_pointers_on_16_byte_boundaries(lbq, m, n, k, rank):
     assert torch.equal(part.codes.double(), ref) and torch.equal(part.scale, rs)
 
 
+@pytest.mark.parametrize("m", [6, 40, 2600])
+@pytest.mark.parametrize("rank", [4, 33])
+def test_an_infinite_factor_stays_with_its_feature(lbq, m, rank):
+    """An infinite element of B (forward) or A (backward) makes its own output feature infinite or NaN and no other."""
+    n, k = 2000, 2000 // 16 * 16
+    codes, scale, A, B = layer(n, k, rank, 3)
+    qw = lbq.Int8Weight(n, k, codes=codes, scale=scale)
+    X, dY = normal((m, k), 1.0, 4), normal((m, n), 0.1, 5)
+    Y0, dX0 = lbq.linear_i8_fwd(X, qw, A, B, 1.0)[0], lbq.linear_i8_bwd(dY, qw, A, B, 1.0)[0]
+    A2, B2 = A.clone(), B.clone()
+    A2[1, 17], B2[130, 1] = float("inf"), float("-inf")
+    Y, dX = lbq.linear_i8_fwd(X, qw, A, B2, 1.0)[0], lbq.linear_i8_bwd(dY, qw, A2, B, 1.0)[0]
+    for got, ref, j in ((Y, Y0, 130), (dX, dX0, 17)):
+        assert not torch.isfinite(got[:, j]).any()
+        got[:, j] = ref[:, j]
+        assert torch.equal(got, ref)
+    assert lbq.device_status() == 0
+
+
 def test_quantized_weight_round_trip(lbq):
     W = normal((300, 528), 0.02, 8)
     qw = lbq.Int8Weight(300, 528).quantize(W)

@@ -56,6 +56,14 @@ def test_bad_arguments(call):
     assert go(ws=0x6008) == lbq.LBQ_EALIGN
 
 
+@pytest.mark.parametrize("call", [lbq.lbq_linear_i8_fwd, lbq.lbq_linear_i8_bwd])
+def test_sixteen_bytes_of_alignment_are_enough(call):
+    """Pointers 16 bytes past a 32-byte boundary pass every check up to the workspace, which comes last."""
+    w = _w(codes=0x1010, scale=0x2010)
+    assert call(0x4010, 4, ctypes.byref(w), 0x7010, 0x8010, 8, 1.0, 0x5010, 0x9010, None, 0, None) == lbq.LBQ_EWORKSPACE
+    assert call(0x4010, 4, ctypes.byref(w), 0x7010, 0x8010, 8, 1.0, 0x5010, 0x9010, 0x6008, WS, None) == lbq.LBQ_EALIGN
+
+
 def test_backward_sizes():
     for n in (100, 131080):                                               # not a multiple of 8; sums past int32
         w = _w(n=n)
